@@ -16,12 +16,18 @@ Entry points (same names as the C ABI):
   right-padded batch of sequences of different lengths
 * ``la_decode_step(q, k, v, S, z, eps=...)`` -> ``o``; S and z updated in place
 * ``la_gated_delta_decode_step(q, k, v, alpha, g, S)`` -> ``o``; S updated in place
+* ``la_causal_conv(x, weight, cache)`` -> ``(out, cache_out)``
+* ``la_ssm_conv(x, weight, bias=..., cache=..., silu=...)`` -> ``(out, cache_out)``,
+  ``la_ssm_scan(x, delta, A, B, C, ...)`` -> ``(y, h)`` and
+  ``la_ssm_step(x, delta, A, B, C, h, ...)`` -> ``y``: the convolution, prompt
+  recurrence and token step of a selective state-space layer
 * ``la_prefill_workspace_bytes(...)``, ``la_prefill_kernel_count(...)``,
   ``la_prefill_varlen_workspace_bytes(...)``,
   ``la_status_string(code)``, ``lib()``
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -37,6 +43,7 @@ EXPORTS = ("la_prefill", "la_prefill_noalloc", "la_prefill_workspace_bytes", "la
            "la_prefill_varlen",
            "la_prefill_varlen_workspace_bytes", "la_decode_step", "la_gated_delta_decode_step",
            "la_set_stage_events", "la_causal_conv", "la_selftest_wait_timeout",
+           "la_ssm_conv", "la_ssm_scan", "la_ssm_scan_workspace_bytes", "la_ssm_step",
            "la_prefill_check", "la_status_string", "la_version")
 
 
@@ -45,6 +52,11 @@ class LaConfig(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int), ("mode", ctypes.c_int), ("eps", ctypes.c_float),
                 ("stream", ctypes.c_void_p), ("S0", ctypes.c_void_p), ("z0", ctypes.c_void_p),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class LaSsmStrides(ctypes.Structure):
+    """Mirror of ``la_ssm_strides`` in include/la.h."""
+    _fields_ = [(f"{t}_{a}", ctypes.c_longlong) for t in ("x", "delta", "z", "B", "C") for a in ("batch", "row")]
 
 
 class LaError(RuntimeError):
@@ -87,6 +99,15 @@ def lib() -> ctypes.CDLL:
         L.la_selftest_wait_timeout.restype = i
         L.la_causal_conv.argtypes = [vp] * 5 + [i] * 5 + [cfgp]
         L.la_causal_conv.restype = i
+        ll, stp = ctypes.c_longlong, ctypes.POINTER(LaSsmStrides)
+        L.la_ssm_conv.argtypes = [vp] * 6 + [ip] + [i] * 5 + [ll] * 2 + [cfgp]
+        L.la_ssm_conv.restype = i
+        L.la_ssm_scan.argtypes = [vp] * 10 + [ip] + [i] * 6 + [stp, cfgp]
+        L.la_ssm_scan.restype = i
+        L.la_ssm_scan_workspace_bytes.argtypes = [i] * 5
+        L.la_ssm_scan_workspace_bytes.restype = ctypes.c_size_t
+        L.la_ssm_step.argtypes = [vp] * 10 + [i] * 5 + [stp, cfgp]
+        L.la_ssm_step.restype = i
         L.la_set_stage_events.argtypes = [ctypes.POINTER(vp), i]
         L.la_set_stage_events.restype = i
         L.la_status_string.argtypes = [i]
@@ -301,6 +322,195 @@ def la_causal_conv(x, weight, cache=None, out=None, cache_out=None, stream=None)
     if rc != LA_OK:
         raise LaError(rc, "la_causal_conv")
     return out, cache_out
+
+
+def _on_device(first, others, stream):
+    """Checks that every tensor is on the first one's CUDA device; returns that
+    device's (given or current) stream handle and the device guard of the call."""
+    torch = _torch()
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("all tensors must be CUDA tensors (the library has no CPU path)")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on one CUDA device, got {dev} and {t.device}")
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    if s.device != dev:
+        raise ValueError(f"the stream is on {s.device}, the tensors on {dev}")
+    return s.cuda_stream, torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else _NO_GUARD
+
+
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _new(shape, dtype, dev, stream):
+    """An output or workspace of a call on ``stream``: it comes from that
+    stream's pool, so that memory still in use elsewhere is not handed out."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, device=dev, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, device=dev, dtype=dtype)
+
+
+def _dense(t, shape, dtype, name):
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _group_of(t, lead, D, name):
+    """(tensor as [..., G, n], G, n) of B or C given as [..., n] or [..., G, n]."""
+    if t.dim() == len(lead) + 1:
+        t = t.unsqueeze(-2)
+    if t.dim() != len(lead) + 2 or t.shape[:-2] != lead:
+        raise ValueError(f"{name} must be [{', '.join(map(str, lead))}, G, n] (or without G), got {list(t.shape)}")
+    G, n = t.shape[-2:]
+    if (n > 1 and t.stride(-1) != 1) or (G > 1 and t.stride(-2) != n):
+        raise ValueError(f"the G * n values of a row of {name} must be contiguous")
+    if G == 0 or D % G:
+        raise ValueError(f"{name} has {G} groups for {D} channels")
+    return t, G, n
+
+
+def _row_stride(t, name):
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    return t.stride(0), t.stride(1) if t.dim() > 2 else 0
+
+
+def _lens_of(seq_lens, B):
+    if seq_lens is None:
+        return None
+    arr, nl = _host_lens(seq_lens)
+    if nl != B:
+        raise ValueError(f"seq_lens has {nl} entries for a batch of {B}")
+    return arr
+
+
+def la_ssm_conv(x, weight, bias=None, cache=None, silu=True, seq_lens=None, out=None, cache_out=None, stream=None):
+    """Short causal convolution of a state-space layer: x [B,N,D] bf16/fp32
+    (batches and rows may be strided), weight [D,w] fp32, bias [D] fp32, cache
+    [B,w-1,D] (the previous inputs; None: zero), seq_lens host ints of a
+    right-padded batch.  Returns ``(out, cache_out)``; cache_out is allocated
+    when not given and may be the cache itself.  One new token is N = 1."""
+    torch = _torch()
+    if x.dim() != 3 or weight.dim() != 2:
+        raise ValueError("x must be [B,N,D] and weight [D,w]")
+    B, N, D = x.shape
+    w = weight.shape[1]
+    xb, xt = _row_stride(x, "x")
+    _dense(weight, (D, w), torch.float32, "weight")
+    if bias is not None:
+        _dense(bias, (D,), torch.float32, "bias")
+    if out is None:
+        out = _new((B, N, D), x.dtype, x.device, stream)
+    if cache_out is None:
+        cache_out = _new((B, w - 1, D), x.dtype, x.device, stream)
+    _dense(out, (B, N, D), x.dtype, "out")
+    _dense(cache_out, (B, w - 1, D), x.dtype, "cache_out")
+    if cache is not None:
+        _dense(cache, (B, w - 1, D), x.dtype, "cache")
+    cfg = LaConfig(_dtype_code(x), 0, 0.0, None, None, None, None, 0)
+    cfg.stream, guard = _on_device(x, (weight, bias, cache, out, cache_out), stream)
+    with guard:
+        rc = lib().la_ssm_conv(_addr(x), _addr(weight), _addr(bias), _addr(cache), _addr(out), _addr(cache_out),
+                               _lens_of(seq_lens, B), B, N, D, w, int(silu), xb, xt, ctypes.byref(cfg))
+    if rc != LA_OK:
+        raise LaError(rc, "la_ssm_conv")
+    return out, cache_out
+
+
+def la_ssm_scan_workspace_bytes(B, N, D, G, n) -> int:
+    return int(lib().la_ssm_scan_workspace_bytes(B, N, D, G, n))
+
+
+def _ssm_checks(x, delta, A, B, C, D, z, delta_bias, rows):
+    """Shapes and strides shared by the prompt scan and the token step."""
+    torch = _torch()
+    ch = x.shape[-1]
+    if delta.shape != x.shape or (z is not None and z.shape != x.shape):
+        raise ValueError(f"delta and z must have the shape of x, {list(x.shape)}")
+    Bt, G, n = _group_of(B, x.shape[:-1], ch, "B")
+    Ct, G2, n2 = _group_of(C, x.shape[:-1], ch, "C")
+    if (G, n) != (G2, n2):
+        raise ValueError(f"B and C differ: {G} x {n} and {G2} x {n2}")
+    for t, name in ((delta, "delta"), (B, "B"), (C, "C"), (z, "z")):
+        if t is not None and t.dtype != x.dtype:
+            raise ValueError(f"x, delta, B, C and z must have one dtype; {name} has {t.dtype}")
+    _dense(A, (ch, n), torch.float32, "A")
+    for t, name in ((D, "D"), (delta_bias, "delta_bias")):
+        if t is not None:
+            _dense(t, (ch,), torch.float32, name)
+    zs = _row_stride(z, "z") if z is not None else (0, 0)
+    bs = (Bt.stride(0), Bt.stride(1) if rows else 0)
+    cs = (Ct.stride(0), Ct.stride(1) if rows else 0)
+    return G, n, LaSsmStrides(*_row_stride(x, "x"), *_row_stride(delta, "delta"), *zs, *bs, *cs)
+
+
+def la_ssm_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, delta_softplus=False, h0=None, seq_lens=None,
+                out=None, h_out=None, workspace=None, stream=None):
+    """Selective state-space recurrence over prompts: x, delta, z [b,N,ch],
+    B, C [b,N,G,n] or [b,N,n] (bf16/fp32, one dtype, rows may be strided), A
+    [ch,n], D, delta_bias [ch] fp32, h0 [b,ch,n] fp32 start states, seq_lens host
+    ints of a right-padded batch.  Returns ``(y, h)`` with the final states."""
+    torch = _torch()
+    if x.dim() != 3:
+        raise ValueError("x must be [B,N,D]")
+    b, N, ch = x.shape
+    G, n, st = _ssm_checks(x, delta, A, B, C, D, z, delta_bias, True)
+    if out is None:
+        out = _new((b, N, ch), x.dtype, x.device, stream)
+    if h_out is None:
+        h_out = _new((b, ch, n), torch.float32, x.device, stream)
+    _dense(out, (b, N, ch), x.dtype, "out")
+    _dense(h_out, (b, ch, n), torch.float32, "h_out")
+    if h0 is not None:
+        _dense(h0, (b, ch, n), torch.float32, "h0")
+    cfg = LaConfig(_dtype_code(x), 0, 0.0, None, _addr(h0), None, None, 0)
+    cfg.stream, guard = _on_device(x, (delta, A, B, C, D, z, delta_bias, h0, out, h_out, workspace), stream)
+    need = la_ssm_scan_workspace_bytes(b, N, ch, G, n)
+    if workspace is None and need > 0:
+        workspace = _new(need, torch.uint8, x.device, stream)
+    if workspace is not None:
+        cfg.workspace = workspace.data_ptr()
+        cfg.workspace_bytes = workspace.numel() * workspace.element_size()
+    with guard:
+        rc = lib().la_ssm_scan(_addr(x), _addr(delta), _addr(A), _addr(B), _addr(C), _addr(D), _addr(z),
+                               _addr(delta_bias), _addr(out), _addr(h_out), _lens_of(seq_lens, b), b, N, ch, G, n,
+                               int(delta_softplus), ctypes.byref(st), ctypes.byref(cfg))
+    if rc != LA_OK:
+        raise LaError(rc, "la_ssm_scan")
+    return out, h_out
+
+
+def la_ssm_step(x, delta, A, B, C, h, D=None, z=None, delta_bias=None, delta_softplus=False, out=None, stream=None):
+    """One token of each sequence: x, delta, z [b,ch]; B, C [b,G,n] or [b,n];
+    h [b,ch,n] fp32 is updated in place.  Other arguments as in
+    ``la_ssm_scan``.  Returns y [b,ch]."""
+    torch = _torch()
+    if x.dim() != 2:
+        raise ValueError("x must be [B,D]")
+    b, ch = x.shape
+    G, n, st = _ssm_checks(x, delta, A, B, C, D, z, delta_bias, False)
+    if out is None:
+        out = _new((b, ch), x.dtype, x.device, stream)
+    _dense(out, (b, ch), x.dtype, "out")
+    _dense(h, (b, ch, n), torch.float32, "h")
+    cfg = LaConfig(_dtype_code(x), 0, 0.0, None, None, None, None, 0)
+    cfg.stream, guard = _on_device(x, (delta, A, B, C, D, z, delta_bias, h, out), stream)
+    with guard:
+        rc = lib().la_ssm_step(_addr(x), _addr(delta), _addr(A), _addr(B), _addr(C), _addr(D), _addr(z),
+                               _addr(delta_bias), _addr(h), _addr(out), b, ch, G, n, int(delta_softplus),
+                               ctypes.byref(st), ctypes.byref(cfg))
+    if rc != LA_OK:
+        raise LaError(rc, "la_ssm_step")
+    return out
 
 
 def la_set_stage_events(events=None):

@@ -158,6 +158,92 @@ la_status run_prefill(const PrefillArgs& a)
     return from_cuda(launch_prefill_simt_kernelized(a));
 }
 
+// ---- state-space layer ---------------------------------------------------------
+
+bool aligned_to(const void* p, size_t e) { return (reinterpret_cast<uintptr_t>(p) % e) == 0; }
+
+// Lengths of a right-padded batch lie inside it.
+bool lens_ok(const int* lens, int B, int N)
+{
+    for (int b = 0; lens && b < B; ++b)
+        if (lens[b] < 0 || lens[b] > N) return false;
+    return true;
+}
+
+// Bytes from the first to past the last element of a [B, N, cols] tensor with these strides.
+size_t extent(int B, int N, long long cols, long long batch, long long row, size_t e)
+{
+    if (B <= 0 || N <= 0 || cols <= 0) return 0;
+    return ((size_t)(B - 1) * batch + (size_t)(N - 1) * row + cols) * e;
+}
+
+// Sequences of one launch: all of them, or kMaxSeqLens where lengths travel with the launch.
+int launch_group(const int* lens) { return lens ? kMaxSeqLens : 32768; }
+
+// Checks shared by la_ssm_scan and la_ssm_step; `tokens` counts the rows of x.
+la_status check_ssm(const void* x, const void* delta, const float* A, const void* Bm, const void* Cm,
+                    const float* D_skip, const void* z, const float* delta_bias, const void* out, const float* h,
+                    long long tokens, int B, int D, int G, int n, const la_ssm_strides* st, const la_config* cfg)
+{
+    if (!cfg || B < 0 || D < 0 || G < 0 || n < 1) return LA_ERR_INVALID;
+    if (cfg->dtype != LA_F32 && cfg->dtype != LA_BF16) return LA_ERR_INVALID;
+    if (n > 64) return LA_ERR_UNSUPPORTED;
+    if (D > 0 && (G == 0 || D % G != 0)) return LA_ERR_INVALID;
+    if ((long long)B * D > 0 && tokens > 0 && (!x || !delta || !A || !Bm || !Cm || !out)) return LA_ERR_INVALID;
+    if (st) {
+        const long long v[] = {st->x_batch, st->x_row, st->delta_batch, st->delta_row, st->z_batch,
+                               st->z_row,   st->B_batch, st->B_row,     st->C_batch,     st->C_row};
+        for (long long k : v)
+            if (k < 0) return LA_ERR_INVALID;
+    }
+    const size_t e = cfg->dtype == LA_BF16 ? 2 : 4;
+    const void* rows[] = {x, delta, Bm, Cm, z, out};
+    for (const void* p : rows)
+        if (!aligned_to(p, e)) return LA_ERR_ALIGN;
+    const void* whole[] = {A, D_skip, delta_bias, h, cfg->S0, cfg->workspace};
+    for (const void* p : whole)
+        if (!aligned16(p)) return LA_ERR_ALIGN;
+    return LA_OK;
+}
+
+SsmArgs ssm_args(const void* x, const void* delta, const float* A, const void* Bm, const void* Cm, const float* D_skip,
+                 const void* z, const float* delta_bias, void* out, float* h, int B, int N, int D, int G, int n,
+                 int softplus, const la_ssm_strides* st, const la_config* cfg)
+{
+    SsmArgs a{};
+    a.x = x; a.delta = delta; a.A = A; a.Bm = Bm; a.Cm = Cm; a.skip = D_skip; a.z = z; a.delta_bias = delta_bias;
+    a.out = out; a.h_out = h;
+    a.B = B; a.N = N; a.D = D; a.G = G; a.n = n;
+    a.softplus = softplus;
+    const long long bc = (long long)G * n;
+    if (st) a.st = *st;
+    else a.st = {(long long)N * D, D, (long long)N * D, D, (long long)N * D, D, N * bc, bc, N * bc, bc};
+    a.dtype = cfg->dtype;
+    a.stream = static_cast<cudaStream_t>(cfg->stream);
+    return a;
+}
+
+// The sequences from b0 on of a batch's arguments.
+SsmArgs ssm_from(SsmArgs a, int b0, int count)
+{
+    const size_t e = a.dtype == LA_BF16 ? 2 : 4;
+    auto move = [&](const void* p, long long stride) {
+        return p ? static_cast<const char*>(p) + (size_t)b0 * stride * e : nullptr;
+    };
+    a.x = move(a.x, a.st.x_batch);
+    a.delta = move(a.delta, a.st.delta_batch);
+    a.z = move(a.z, a.st.z_batch);
+    a.Bm = move(a.Bm, a.st.B_batch);
+    a.Cm = move(a.Cm, a.st.C_batch);
+    a.out = const_cast<char*>(move(a.out, (long long)a.N * a.D));
+    const size_t states = (size_t)b0 * a.D * a.n;
+    if (a.h0) a.h0 += states;
+    if (a.h_out) a.h_out += states;
+    if (a.seq_lens) a.seq_lens += b0;
+    a.B = count;
+    return a;
+}
+
 }  // namespace
 }  // namespace la
 
@@ -395,6 +481,106 @@ la_status la_causal_conv(const void* x, const float* weight, const void* cache, 
     a.stream = static_cast<cudaStream_t>(cfg->stream);
     if (a.N == 0 && !a.cache_out) return LA_OK;
     return la::from_cuda(la::launch_causal_conv(a));
+}
+
+la_status la_ssm_conv(const void* x, const float* weight, const float* bias, const void* cache, void* out,
+                      void* cache_out, const int* seq_lens, int B, int N, int D, int w, int silu, long long x_batch,
+                      long long x_row, const la_config* cfg)
+{
+    if (!cfg) return LA_ERR_INVALID;
+    if (B < 0 || N < 0 || D < 0 || w < 1 || x_batch < 0 || x_row < 0) return LA_ERR_INVALID;
+    if (cfg->dtype != LA_F32 && cfg->dtype != LA_BF16) return LA_ERR_INVALID;
+    if (w > 8) return LA_ERR_UNSUPPORTED;
+    if (!la::lens_ok(seq_lens, B, N)) return LA_ERR_INVALID;
+    if (B == 0 || D == 0) return LA_OK;
+    if (N > 0 && (!x || !weight || !out)) return LA_ERR_INVALID;
+    const size_t e = cfg->dtype == LA_BF16 ? 2 : 4;
+    const size_t cache_bytes = (size_t)B * (w - 1) * D * e;
+    if (cache_out != cache && la::overlap(cache_out, cache_bytes, cache, cache_bytes)) return LA_ERR_INVALID;
+    if (la::overlap(cache_out, cache_bytes, x, la::extent(B, N, D, x_batch, x_row, e))) return LA_ERR_INVALID;
+    const void* rows[] = {x, cache, out, cache_out};
+    for (const void* p : rows)
+        if (!la::aligned_to(p, e)) return LA_ERR_ALIGN;
+    if (!la::aligned16(weight) || !la::aligned16(bias)) return LA_ERR_ALIGN;
+    if (w == 1) cache = cache_out = nullptr;
+    if (N == 0 && !cache_out) return LA_OK;
+    const int step = la::launch_group(seq_lens);
+    for (int b0 = 0; b0 < B; b0 += step) {
+        la::SsmConvArgs a{};
+        const size_t rows0 = (size_t)b0 * D * e;
+        auto move = [&](const void* p, size_t by) { return p ? static_cast<const char*>(p) + by : nullptr; };
+        a.x = move(x, (size_t)b0 * x_batch * e);
+        a.weight = weight;
+        a.bias = bias;
+        a.cache = move(cache, rows0 * (w - 1));
+        a.out = const_cast<char*>(move(out, rows0 * N));
+        a.cache_out = const_cast<char*>(move(cache_out, rows0 * (w - 1)));
+        a.seq_lens = seq_lens ? seq_lens + b0 : nullptr;
+        a.B = B - b0 < step ? B - b0 : step;
+        a.N = N; a.D = D; a.w = w;
+        a.silu = silu;
+        a.x_batch = x_batch; a.x_row = x_row;
+        a.dtype = cfg->dtype;
+        a.stream = static_cast<cudaStream_t>(cfg->stream);
+        const cudaError_t err = la::launch_ssm_conv(a);
+        if (err != cudaSuccess) return LA_ERR_CUDA;
+        if (b0 == 0) la::stage_mark(0, a.stream);
+    }
+    return LA_OK;
+}
+
+size_t la_ssm_scan_workspace_bytes(int B, int N, int D, int G, int n)
+{
+    if (B <= 0 || N <= 0 || D <= 0 || G <= 0 || D % G != 0 || n < 1 || n > 64) return 0;
+    return la::ssm_scan_workspace_bytes(B, N, D, G, n);
+}
+
+la_status la_ssm_scan(const void* x, const void* delta, const float* A, const void* Bm, const void* Cm,
+                      const float* D_skip, const void* z, const float* delta_bias, void* out, float* h_out,
+                      const int* seq_lens, int B, int N, int D, int G, int n, int delta_softplus,
+                      const la_ssm_strides* strides, const la_config* cfg)
+{
+    if (N < 0) return LA_ERR_INVALID;
+    const la_status st =
+        la::check_ssm(x, delta, A, Bm, Cm, D_skip, z, delta_bias, out, h_out, N, B, D, G, n, strides, cfg);
+    if (st != LA_OK) return st;
+    if (!la::lens_ok(seq_lens, B, N)) return LA_ERR_INVALID;
+    const size_t states = (size_t)B * D * n * sizeof(float);
+    if (la::overlap(h_out, states, cfg->S0, states)) return LA_ERR_INVALID;
+    if (cfg->workspace_bytes < la_ssm_scan_workspace_bytes(B, N, D, G, n)) return LA_ERR_WORKSPACE;
+    if (B == 0 || D == 0) return LA_OK;
+    cudaStream_t stream = static_cast<cudaStream_t>(cfg->stream);
+    if (N == 0) {
+        if (!h_out) return LA_OK;
+        return la::from_cuda(cfg->S0 ? cudaMemcpyAsync(h_out, cfg->S0, states, cudaMemcpyDeviceToDevice, stream)
+                                     : cudaMemsetAsync(h_out, 0, states, stream));
+    }
+    la::SsmArgs all = la::ssm_args(x, delta, A, Bm, Cm, D_skip, z, delta_bias, out, h_out, B, N, D, G, n,
+                                   delta_softplus, strides, cfg);
+    all.h0 = cfg->S0;
+    all.seq_lens = seq_lens;
+    la::ssm_scan_segments(B, N, D, G, n, &all.segs, &all.seg_len);
+    const size_t per = la_ssm_scan_workspace_bytes(B, N, D, G, n) / B / sizeof(float);
+    const int step = la::launch_group(seq_lens);
+    for (int b0 = 0; b0 < B; b0 += step) {
+        la::SsmArgs a = la::ssm_from(all, b0, B - b0 < step ? B - b0 : step);
+        if (per) a.workspace = static_cast<float*>(cfg->workspace) + (size_t)b0 * per;
+        const cudaError_t err = la::launch_ssm_scan(a);
+        if (err != cudaSuccess) return LA_ERR_CUDA;
+    }
+    return LA_OK;
+}
+
+la_status la_ssm_step(const void* x, const void* delta, const float* A, const void* Bm, const void* Cm,
+                      const float* D_skip, const void* z, const float* delta_bias, float* h, void* out, int B, int D,
+                      int G, int n, int delta_softplus, const la_ssm_strides* strides, const la_config* cfg)
+{
+    const la_status st = la::check_ssm(x, delta, A, Bm, Cm, D_skip, z, delta_bias, out, h, 1, B, D, G, n, strides, cfg);
+    if (st != LA_OK) return st;
+    if (B == 0 || D == 0) return LA_OK;
+    if (!h) return LA_ERR_INVALID;
+    return la::from_cuda(la::launch_ssm_step(
+        la::ssm_args(x, delta, A, Bm, Cm, D_skip, z, delta_bias, out, h, B, 1, D, G, n, delta_softplus, strides, cfg)));
 }
 
 la_status la_set_stage_events(void* const* events, int n)

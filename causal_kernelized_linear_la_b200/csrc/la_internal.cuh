@@ -66,7 +66,58 @@ struct ConvArgs {
     cudaStream_t stream;
 };
 
+// Lengths of the sequences of one launch travel as kernel parameters; a longer
+// batch with lengths runs as several launches.
+constexpr int kMaxSeqLens = 128;
+
+// One launch's sequences of la_ssm_conv (strides in elements).
+struct SsmConvArgs {
+    const void* x;
+    const float* weight;
+    const float* bias;      // may be null
+    const void* cache;      // may be null: zero history
+    void* out;
+    void* cache_out;        // may be null
+    const int* seq_lens;    // host, B of them, or null: every sequence holds N tokens
+    int B, N, D, w;
+    int silu;
+    long long x_batch, x_row;
+    la_dtype dtype;
+    cudaStream_t stream;
+};
+
+// One launch's sequences of la_ssm_scan, or (N = 1, h = h_out in place) of la_ssm_step.
+struct SsmArgs {
+    const void* x;
+    const void* delta;
+    const float* A;          // [D, n]
+    const void* Bm;
+    const void* Cm;
+    const float* skip;       // [D] or null
+    const void* z;           // or null
+    const float* delta_bias; // [D] or null
+    void* out;
+    const float* h0;         // [B, D, n] or null
+    float* h_out;            // [B, D, n]
+    const int* seq_lens;     // host, or null
+    int B, N, D, G, n;
+    int softplus;
+    la_ssm_strides st;
+    la_dtype dtype;
+    cudaStream_t stream;
+    float* workspace;
+    int segs, seg_len;       // segments of a sequence and their length (a multiple of the token tile)
+};
+
 bool uses_tc_kernelized(la_dtype dt, la_mode m);
+
+// Selective state-space layer: convolution, prompt scan, token step.
+cudaError_t launch_ssm_conv(const SsmConvArgs& a);
+cudaError_t launch_ssm_scan(const SsmArgs& a);
+cudaError_t launch_ssm_step(const SsmArgs& a);
+// segments of a prompt scan, their length, and the bytes of their summaries
+void ssm_scan_segments(int B, int N, int D, int G, int n, int* segs, int* seg_len);
+size_t ssm_scan_workspace_bytes(int B, int N, int D, int G, int n);
 
 // Short causal convolution with conv cache (memory-bound SIMT).
 cudaError_t launch_causal_conv(const ConvArgs& a);

@@ -300,9 +300,107 @@ LA_API la_status la_causal_conv(const void* x, const float* weight, const void* 
                                 int B, int H, int N, int d, int w, const la_config* cfg);
 
 /*
+ * Selective state-space layer: the token mixer whose state decays per channel
+ * and state by an input-dependent step.  Three entry points make the layer: a
+ * short causal convolution with bias and SiLU, the recurrence over prompts and
+ * the recurrence for one token a sequence.  Conventions that differ from the
+ * attention entry points:
+ * - Rows are token-major: x, delta, z, out [B,N,D]; B, C [B,N,G,n]; channel c
+ *   uses group c / (D / G) of B and C.  The innermost axis (G*n for B and C) is
+ *   dense; batches and rows may be strided, so that parts of one projection's
+ *   output are passed in place.  out is dense.
+ * - x, delta, z, B, C, the convolution's cache and out share the type
+ *   cfg->dtype; A, D_skip, delta_bias, weight, bias and states are fp32.
+ * - x, delta, z, B, C, out and the convolution's caches need the alignment of
+ *   their elements only (16-byte aligned rows run faster); states, A, weight,
+ *   bias, D_skip, delta_bias and the workspace are 16-byte aligned.
+ * - seq_lens is a HOST array of B lengths of a right-padded batch, each
+ *   0 <= seq_lens[b] <= N, or NULL (every sequence holds N tokens).  Padding rows
+ *   never reach a result, whatever they hold; padding rows of out are not written.
+ * - B, N, G >= 0 and D >= 0 of any size with D a multiple of G; 1 <= n <= 64.
+ */
+
+/* Strides in elements (>= 0) of the rows of a state-space call; NULL in place
+ * of this struct means dense [B,N,D] and [B,N,G,n].  la_ssm_step reads the
+ * batch strides only. */
+typedef struct {
+    long long x_batch, x_row;
+    long long delta_batch, delta_row;
+    long long z_batch, z_row;
+    long long B_batch, B_row;
+    long long C_batch, C_row;
+} la_ssm_strides;
+
+/*
+ * la_ssm_conv -- short causal convolution of a state-space layer, with
+ * xh = [cache; x] along the tokens:
+ *
+ *   out_t[c] = act(bias[c] + sum_{i=0}^{w-1} weight[c][i] * xh[t + i][c])
+ *
+ * cache_out = the last w-1 rows of each sequence's xh.
+ *
+ *   x          [B,N,D], batch and row strides x_batch, x_row (elements).
+ *   weight     [D,w] fp32; the last tap multiplies the current token.
+ *   bias       [D] fp32 or NULL.
+ *   cache      [B,w-1,D] previous inputs, or NULL for zero history.
+ *   out        [B,N,D]; fp32 arithmetic, rounded once.
+ *   cache_out  [B,w-1,D] or NULL.  May be the cache itself (updated in place);
+ *              any other overlap with cache, and any with x, is LA_ERR_INVALID.
+ *   silu       0: act is the identity; 1: act(y) = y / (1 + exp(-y)).
+ *   w          1..8.
+ *   cfg        dtype and stream are used.
+ *
+ * One new token is the N = 1 call.  LA_ERR_INVALID for bad sizes, lengths,
+ * strides, overlaps or missing pointers; LA_ERR_UNSUPPORTED for w > 8;
+ * LA_ERR_ALIGN.
+ */
+LA_API la_status la_ssm_conv(const void* x, const float* weight, const float* bias, const void* cache,
+                             void* out, void* cache_out, const int* seq_lens, int B, int N, int D, int w, int silu,
+                             long long x_batch, long long x_row, const la_config* cfg);
+
+/*
+ * la_ssm_scan -- the recurrence over prompts, from a zero or a given state:
+ *
+ *   dt_t = delta_t[c] + delta_bias[c], then softplus if delta_softplus
+ *   h_t[c][s] = exp(dt_t A[c][s]) h_{t-1}[c][s] + dt_t x_t[c] B_t[s]
+ *   y_t[c]    = (sum_s C_t[s] h_t[c][s] + D_skip[c] x_t[c]) * silu(z_t[c])
+ *
+ *   A          [D,n] fp32 (negative for a decaying state).
+ *   D_skip, delta_bias  [D] fp32 or NULL (no skip term, no bias).
+ *   z          the gate, or NULL (no gate).
+ *   out        y [B,N,D].
+ *   h_out      final states [B,D,n] fp32 or NULL; a sequence of length 0 reports its start state.
+ *   cfg        dtype, stream; S0 = start states [B,D,n] fp32 or NULL (zero);
+ *              workspace of la_ssm_scan_workspace_bytes() bytes.  h_out must not
+ *              share a byte with S0 (LA_ERR_INVALID): alternate two buffers.
+ *
+ * All arithmetic is fp32.  LA_ERR_INVALID, LA_ERR_UNSUPPORTED (n > 64),
+ * LA_ERR_ALIGN, LA_ERR_WORKSPACE as elsewhere.
+ */
+LA_API la_status la_ssm_scan(const void* x, const void* delta, const float* A, const void* Bm, const void* Cm,
+                             const float* D_skip, const void* z, const float* delta_bias, void* out, float* h_out,
+                             const int* seq_lens, int B, int N, int D, int G, int n, int delta_softplus,
+                             const la_ssm_strides* strides, const la_config* cfg);
+
+/* Device scratch of la_ssm_scan for these sizes; 0 when the tokens run in one segment. */
+LA_API size_t la_ssm_scan_workspace_bytes(int B, int N, int D, int G, int n);
+
+/*
+ * la_ssm_step -- one token of each of B sequences against resident states: the
+ * recurrence of la_ssm_scan with N = 1, x, delta, z, out [B,D]; B, C [B,G,n].
+ *
+ *   h          [B,D,n] fp32, read and updated in place.
+ *   cfg        dtype and stream are used.
+ */
+LA_API la_status la_ssm_step(const void* x, const void* delta, const float* A, const void* Bm, const void* Cm,
+                             const float* D_skip, const void* z, const float* delta_bias, float* h, void* out,
+                             int B, int D, int G, int n, int delta_softplus, const la_ssm_strides* strides,
+                             const la_config* cfg);
+
+/*
  * la_set_stage_events -- profiling hook, off by default.  With n > 0, every
  * later la_prefill / la_decode_step / la_gated_delta_decode_step /
- * la_causal_conv records
+ * la_causal_conv / la_ssm_conv / la_ssm_scan / la_ssm_step records
  * events[i] on its cfg->stream right after launching its i-th kernel
  * (i < n; a call launches 1 to 16 kernels, la_prefill_kernel_count gives the
  * number for a prefill: bf16 LA_PLAIN/LA_DECAY prefill = segment summaries,
