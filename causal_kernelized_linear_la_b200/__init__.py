@@ -21,6 +21,9 @@ Entry points (same names as the C ABI):
   ``la_ssm_scan(x, delta, A, B, C, ...)`` -> ``(y, h)`` and
   ``la_ssm_step(x, delta, A, B, C, h, ...)`` -> ``y``: the convolution, prompt
   recurrence and token step of a selective state-space layer
+* ``la_window_prefill(q, k, v, window, sinks=..., k_cache=..., v_cache=..., pos=...)``
+  -> ``o`` and ``la_window_decode_step(q, k, v, k_cache, v_cache, pos, window, ...)``
+  -> ``o``: sliding-window attention with sinks; the rolling caches are updated in place
 * ``la_prefill_workspace_bytes(...)``, ``la_prefill_kernel_count(...)``,
   ``la_prefill_varlen_workspace_bytes(...)``,
   ``la_status_string(code)``, ``lib()``
@@ -44,6 +47,7 @@ EXPORTS = ("la_prefill", "la_prefill_noalloc", "la_prefill_workspace_bytes", "la
            "la_prefill_varlen_workspace_bytes", "la_decode_step", "la_gated_delta_decode_step",
            "la_set_stage_events", "la_causal_conv", "la_selftest_wait_timeout",
            "la_ssm_conv", "la_ssm_scan", "la_ssm_scan_workspace_bytes", "la_ssm_step",
+           "la_window_prefill", "la_window_decode_step",
            "la_prefill_check", "la_status_string", "la_version")
 
 
@@ -57,6 +61,11 @@ class LaConfig(ctypes.Structure):
 class LaSsmStrides(ctypes.Structure):
     """Mirror of ``la_ssm_strides`` in include/la.h."""
     _fields_ = [(f"{t}_{a}", ctypes.c_longlong) for t in ("x", "delta", "z", "B", "C") for a in ("batch", "row")]
+
+
+class LaWindowStrides(ctypes.Structure):
+    """Mirror of ``la_window_strides`` in include/la.h."""
+    _fields_ = [(f"{t}_{a}", ctypes.c_longlong) for t in ("q", "k", "v", "out") for a in ("batch", "head", "row")]
 
 
 class LaError(RuntimeError):
@@ -108,6 +117,11 @@ def lib() -> ctypes.CDLL:
         L.la_ssm_scan_workspace_bytes.restype = ctypes.c_size_t
         L.la_ssm_step.argtypes = [vp] * 10 + [i] * 5 + [stp, cfgp]
         L.la_ssm_step.restype = i
+        wsp, fl = ctypes.POINTER(LaWindowStrides), ctypes.c_float
+        L.la_window_prefill.argtypes = [vp] * 7 + [ip] + [i] * 8 + [fl, wsp, cfgp]
+        L.la_window_prefill.restype = i
+        L.la_window_decode_step.argtypes = [vp] * 7 + [i] * 7 + [fl, wsp, cfgp]
+        L.la_window_decode_step.restype = i
         L.la_set_stage_events.argtypes = [ctypes.POINTER(vp), i]
         L.la_set_stage_events.restype = i
         L.la_status_string.argtypes = [i]
@@ -381,7 +395,8 @@ def _group_of(t, lead, D, name):
 def _row_stride(t, name):
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"the last axis of {name} must be contiguous")
-    return t.stride(0), t.stride(1) if t.dim() > 2 else 0
+    # an axis of one entry has no stride that matters
+    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.dim() > 2 and t.shape[1] > 1 else 0
 
 
 def _lens_of(seq_lens, B):
@@ -448,8 +463,7 @@ def _ssm_checks(x, delta, A, B, C, D, z, delta_bias, rows):
         if t is not None:
             _dense(t, (ch,), torch.float32, name)
     zs = _row_stride(z, "z") if z is not None else (0, 0)
-    bs = (Bt.stride(0), Bt.stride(1) if rows else 0)
-    cs = (Ct.stride(0), Ct.stride(1) if rows else 0)
+    bs, cs = ((t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if rows and t.shape[1] > 1 else 0) for t in (Bt, Ct))
     return G, n, LaSsmStrides(*_row_stride(x, "x"), *_row_stride(delta, "delta"), *zs, *bs, *cs)
 
 
@@ -510,6 +524,76 @@ def la_ssm_step(x, delta, A, B, C, h, D=None, z=None, delta_bias=None, delta_sof
                                ctypes.byref(st), ctypes.byref(cfg))
     if rc != LA_OK:
         raise LaError(rc, "la_ssm_step")
+    return out
+
+
+def _window_checks(q, k, v, out, k_cache, v_cache, pos, window, sinks, scale):
+    """Shapes of both window calls (trailing axes; decode has no token axis)."""
+    torch = _torch()
+    B, Hq, d = q.shape[0], q.shape[1], q.shape[-1]
+    Hkv, dv = k.shape[1], v.shape[-1]
+    if k.shape != (B, Hkv, *q.shape[2:]) or v.shape != (B, Hkv, *q.shape[2:-1], dv):
+        raise ValueError(f"q, k, v do not fit: {list(q.shape)}, {list(k.shape)}, {list(v.shape)}")
+    if out.shape != (*q.shape[:-1], dv):
+        raise ValueError(f"out must be {[*q.shape[:-1], dv]}, got {list(out.shape)}")
+    if not q.dtype == k.dtype == v.dtype == out.dtype:
+        raise ValueError("q, k, v and out must have one dtype")
+    st = []
+    for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
+        if t.stride(-1) != 1:
+            raise ValueError(f"the last axis of {name} must be contiguous")
+        # an axis of one entry has no stride that matters
+        st += [s if n > 1 else 0 for s, n in zip(t.stride()[:-1], t.shape[:-1])] + [0] * (4 - t.dim())
+    if k_cache is not None:
+        _dense(k_cache, (B, Hkv, sinks + window, d), q.dtype, "k_cache")
+    if v_cache is not None:
+        _dense(v_cache, (B, Hkv, sinks + window, dv), q.dtype, "v_cache")
+    if pos is not None:
+        _dense(pos, (B,), torch.int32, "pos")
+    return B, Hq, Hkv, d, dv, float(d ** -0.5 if scale is None else scale), LaWindowStrides(*st)
+
+
+def la_window_prefill(q, k, v, window, sinks=0, k_cache=None, v_cache=None, pos=None, seq_lens=None, scale=None,
+                      out=None, stream=None):
+    """Sliding-window attention with sinks over prompts: q [B,Hq,N,d], k
+    [B,Hkv,N,d], v [B,Hkv,N,dv] (bf16/fp32; batches, heads and rows may be
+    strided).  With the rolling caches [B,Hkv,sinks+window,.] the tokens follow
+    the pos[b] (int32, on the device; None: 0) cached ones and the caches are
+    updated in place; pos itself is not.  seq_lens: host ints of a right-padded
+    batch.  scale defaults to d ** -0.5.  Returns o [B,Hq,N,dv]."""
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be [B,Hq,N,d], k [B,Hkv,N,d] and v [B,Hkv,N,dv]")
+    if out is None:
+        out = _new((*q.shape[:-1], v.shape[-1]), q.dtype, q.device, stream)
+    B, Hq, Hkv, d, dv, scale, st = _window_checks(q, k, v, out, k_cache, v_cache, pos, window, sinks, scale)
+    cfg = LaConfig(_dtype_code(q), 0, 0.0, None, None, None, None, 0)
+    cfg.stream, guard = _on_device(q, (k, v, out, k_cache, v_cache, pos), stream)
+    with guard:
+        rc = lib().la_window_prefill(_addr(q), _addr(k), _addr(v), _addr(out), _addr(k_cache), _addr(v_cache),
+                                     _addr(pos), _lens_of(seq_lens, B), B, Hq, Hkv, q.shape[2], d, dv, window, sinks,
+                                     scale, ctypes.byref(st), ctypes.byref(cfg))
+    if rc != LA_OK:
+        raise LaError(rc, "la_window_prefill")
+    return out
+
+
+def la_window_decode_step(q, k, v, k_cache, v_cache, pos, window, sinks=0, scale=None, out=None, stream=None):
+    """One token of each sequence: q [B,Hq,d], k [B,Hkv,d], v [B,Hkv,dv] at
+    position pos[b] (int32, on the device; negative: an idle sequence).  The
+    caches take k and v in place.  Returns o [B,Hq,dv]."""
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q must be [B,Hq,d], k [B,Hkv,d] and v [B,Hkv,dv]")
+    if out is None:
+        out = _new((*q.shape[:-1], v.shape[-1]), q.dtype, q.device, stream)
+    B, Hq, Hkv, d, dv, scale, st = _window_checks(q, k, v, out, k_cache, v_cache, pos, window, sinks, scale)
+    cfg = LaConfig(_dtype_code(q), 0, 0.0, None, None, None, None, 0)
+    cfg.stream, guard = _on_device(q, (k, v, out, k_cache, v_cache, pos), stream)
+    with guard:
+        rc = lib().la_window_decode_step(_addr(q), _addr(k), _addr(v), _addr(out), _addr(k_cache), _addr(v_cache),
+                                         _addr(pos), B, Hq, Hkv, d, dv, window, sinks, scale, ctypes.byref(st),
+                                         ctypes.byref(cfg))
+    if rc != LA_OK:
+        raise LaError(rc, "la_window_decode_step")
     return out
 
 

@@ -4,6 +4,7 @@
 
 #include "la_internal.cuh"
 #include "la_prefill_tc.cuh"
+#include "la_window.cuh"
 
 namespace la {
 namespace {
@@ -239,6 +240,88 @@ SsmArgs ssm_from(SsmArgs a, int b0, int count)
     const size_t states = (size_t)b0 * a.D * a.n;
     if (a.h0) a.h0 += states;
     if (a.h_out) a.h_out += states;
+    if (a.seq_lens) a.seq_lens += b0;
+    a.B = count;
+    return a;
+}
+
+// ---- sliding-window attention --------------------------------------------------
+
+// Bytes from the first to past the last element of a [B, H, N, cols] tensor.
+size_t extent4(int B, int H, int N, int cols, long long batch, long long head, long long row, size_t e)
+{
+    if (B <= 0 || H <= 0 || N <= 0) return 0;
+    return ((size_t)(B - 1) * batch + (size_t)(H - 1) * head + (size_t)(N - 1) * row + cols) * e;
+}
+
+// Checks shared by la_window_prefill and la_window_decode_step (N = 1); fills the arguments.
+la_status check_window(WindowArgs* w, const void* q, const void* k, const void* v, void* out, void* k_cache,
+                       void* v_cache, const int* pos, int B, int Hq, int Hkv, int N, int d, int dv, int window,
+                       int sinks, float scale, const la_window_strides* st, const la_config* cfg)
+{
+    if (!cfg || B < 0 || Hq < 0 || Hkv < 0 || N < 0 || window < 1 || sinks < 0) return LA_ERR_INVALID;
+    if (cfg->dtype != LA_F32 && cfg->dtype != LA_BF16) return LA_ERR_INVALID;
+    if (!head_ok(d) || !head_ok(dv)) return LA_ERR_UNSUPPORTED;
+    if ((long long)window + sinks > 0x7fffffffLL) return LA_ERR_INVALID;
+    if (Hq > 0 && (Hkv == 0 || Hq % Hkv != 0)) return LA_ERR_INVALID;
+    if (Hq > 65535) return LA_ERR_UNSUPPORTED;
+    if (!(scale == scale) || scale - scale != 0.f) return LA_ERR_INVALID;   // NaN or infinite
+    if ((k_cache == nullptr) != (v_cache == nullptr)) return LA_ERR_INVALID;
+    const long long work = (long long)B * Hq * N;
+    if (work > 0 && (!q || !k || !v || !out)) return LA_ERR_INVALID;
+    la_window_strides s{(long long)Hq * N * d,  (long long)N * d,  d,  (long long)Hkv * N * d, (long long)N * d,  d,
+                        (long long)Hkv * N * dv, (long long)N * dv, dv, (long long)Hq * N * dv, (long long)N * dv, dv};
+    if (st) s = *st;
+    const size_t e = cfg->dtype == LA_BF16 ? 2 : 4;
+    const long long strides[] = {s.q_batch, s.q_head, s.q_row, s.k_batch, s.k_head, s.k_row,
+                                 s.v_batch, s.v_head, s.v_row, s.out_batch, s.out_head, s.out_row};
+    for (long long x : strides) {
+        if (x < 0) return LA_ERR_INVALID;
+        if (x * (long long)e % 16 != 0) return LA_ERR_ALIGN;
+    }
+    const void* ptrs[] = {q, k, v, out, k_cache, v_cache};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return LA_ERR_ALIGN;
+    if (!aligned_to(pos, sizeof(int))) return LA_ERR_ALIGN;
+    if (work > 0) {
+        const size_t cap = (size_t)window + sinks;
+        const size_t ks = extent4(B, Hkv, N, d, s.k_batch, s.k_head, s.k_row, e);
+        const size_t vs = extent4(B, Hkv, N, dv, s.v_batch, s.v_head, s.v_row, e);
+        const size_t os = extent4(B, Hq, N, dv, s.out_batch, s.out_head, s.out_row, e);
+        const void* written[] = {out, k_cache, v_cache};
+        const size_t wn[] = {os, (size_t)B * Hkv * cap * d * e, (size_t)B * Hkv * cap * dv * e};
+        for (int i = 0; i < 3; ++i) {
+            // strided k and v may interleave with a strided out inside one buffer: only dense ranges are compared
+            if (!st && (overlap(written[i], wn[i], k, ks) || overlap(written[i], wn[i], v, vs))) return LA_ERR_INVALID;
+            if (i > 0 && (overlap(written[i], wn[i], k, ks) || overlap(written[i], wn[i], v, vs))) return LA_ERR_INVALID;
+        }
+        if (overlap(k_cache, wn[1], v_cache, wn[2])) return LA_ERR_INVALID;
+    }
+    *w = WindowArgs{};
+    w->q = q; w->k = k; w->v = v; w->out = out; w->k_cache = k_cache; w->v_cache = v_cache; w->pos = pos;
+    w->B = B; w->Hq = Hq; w->Hkv = Hkv; w->N = N; w->d = d; w->dv = dv;
+    w->window = window; w->sinks = sinks; w->scale = scale;
+    w->st = s;
+    w->dtype = cfg->dtype;
+    w->stream = static_cast<cudaStream_t>(cfg->stream);
+    return LA_OK;
+}
+
+// The sequences from b0 on.
+WindowArgs window_from(WindowArgs a, int b0, int count)
+{
+    const size_t e = a.dtype == LA_BF16 ? 2 : 4;
+    auto move = [&](const void* p, long long stride) {
+        return p ? const_cast<char*>(static_cast<const char*>(p)) + (size_t)b0 * stride * e : nullptr;
+    };
+    const long long cap = (long long)a.window + a.sinks;
+    a.q = move(a.q, a.st.q_batch);
+    a.k = move(a.k, a.st.k_batch);
+    a.v = move(a.v, a.st.v_batch);
+    a.out = move(a.out, a.st.out_batch);
+    a.k_cache = move(a.k_cache, a.Hkv * cap * a.d);
+    a.v_cache = move(a.v_cache, a.Hkv * cap * a.dv);
+    if (a.pos) a.pos += b0;
     if (a.seq_lens) a.seq_lens += b0;
     a.B = count;
     return a;
@@ -581,6 +664,51 @@ la_status la_ssm_step(const void* x, const void* delta, const float* A, const vo
     if (!h) return LA_ERR_INVALID;
     return la::from_cuda(la::launch_ssm_step(
         la::ssm_args(x, delta, A, Bm, Cm, D_skip, z, delta_bias, out, h, B, 1, D, G, n, delta_softplus, strides, cfg)));
+}
+
+la_status la_window_prefill(const void* q, const void* k, const void* v, void* out, void* k_cache, void* v_cache,
+                            const int* pos, const int* seq_lens, int B, int Hq, int Hkv, int N, int d, int dv,
+                            int window, int sinks, float scale, const la_window_strides* strides, const la_config* cfg)
+{
+    la::WindowArgs all;
+    const la_status st = la::check_window(&all, q, k, v, out, k_cache, v_cache, pos, B, Hq, Hkv, N, d, dv, window,
+                                          sinks, scale, strides, cfg);
+    if (st != LA_OK) return st;
+    if (pos && !k_cache) return LA_ERR_INVALID;
+    if (!la::lens_ok(seq_lens, B, N)) return LA_ERR_INVALID;
+    if ((long long)B * Hq * N == 0) return LA_OK;
+    all.seq_lens = seq_lens;
+    const int step = la::launch_group(seq_lens);
+    for (int b0 = 0; b0 < B; b0 += step) {
+        const la::WindowArgs a = la::window_from(all, b0, B - b0 < step ? B - b0 : step);
+        cudaError_t err = la::launch_window_prefill_simt(a);
+        if (err == cudaSuccess) la::stage_mark(0, a.stream);
+        if (err == cudaSuccess && a.k_cache) {
+            err = la::launch_window_cache_update(a);
+            if (err == cudaSuccess) la::stage_mark(1, a.stream);
+        }
+        if (err != cudaSuccess) return LA_ERR_CUDA;
+    }
+    return LA_OK;
+}
+
+la_status la_window_decode_step(const void* q, const void* k, const void* v, void* out, void* k_cache, void* v_cache,
+                                const int* pos, int B, int Hq, int Hkv, int d, int dv, int window, int sinks,
+                                float scale, const la_window_strides* strides, const la_config* cfg)
+{
+    la::WindowArgs all;
+    const la_status st = la::check_window(&all, q, k, v, out, k_cache, v_cache, pos, B, Hq, Hkv, 1, d, dv, window,
+                                          sinks, scale, strides, cfg);
+    if (st != LA_OK) return st;
+    if ((long long)B * Hq == 0) return LA_OK;
+    if (!k_cache || !pos) return LA_ERR_INVALID;
+    const int step = la::launch_group(nullptr);
+    for (int b0 = 0; b0 < B; b0 += step) {
+        const la::WindowArgs a = la::window_from(all, b0, B - b0 < step ? B - b0 : step);
+        if (la::launch_window_decode(a) != cudaSuccess) return LA_ERR_CUDA;
+        la::stage_mark(0, a.stream);
+    }
+    return LA_OK;
 }
 
 la_status la_set_stage_events(void* const* events, int n)

@@ -398,9 +398,78 @@ LA_API la_status la_ssm_step(const void* x, const void* delta, const float* A, c
                              const la_config* cfg);
 
 /*
+ * Sliding-window attention with sinks: softmax attention whose context, like a
+ * linear layer's state, stays bounded.  The token at position p sees itself,
+ * the window - 1 tokens before it and every token at a position below sinks:
+ *
+ *   o_i = sum_j w_ij v_j / sum_j w_ij,  w_ij = exp(scale q_i.k_j),
+ *   over j <= i with i - j < window or j < sinks
+ *
+ * The rolling cache k_cache [B,Hkv,sinks+window,d], v_cache
+ * [B,Hkv,sinks+window,dv] (cfg->dtype, dense) has a slot for each sink and
+ * `window` ring slots: position p lives in slot p (p < sinks) or
+ * sinks + (p - sinks) mod window.  pos [B] is a DEVICE array of int32: the
+ * number of tokens of each sequence already in the cache, which is also the
+ * position of its first new token.  A negative entry marks an idle sequence:
+ * nothing of it is read, its rows of out and of the cache stay as they are.
+ * The calls do not change pos, and slots not yet filled never reach a result.
+ *
+ * Query head h reads kv head h / (Hq / Hkv); Hq is a multiple of Hkv.  d, dv in
+ * {64, 128}; window >= 1, sinks >= 0, sinks + window < 2^31; positions stay
+ * below 2^31.  Sums, maxima and outputs accumulate in fp32.  All pointers are
+ * 16-byte aligned, and so are the rows (strides are multiples of 16 bytes).
+ */
+
+/* Strides in elements (>= 0); NULL in place of this struct means dense
+ * [B,H,N,.] (prefill) or [B,H,.] (decode, which reads no row strides). */
+typedef struct {
+    long long q_batch, q_head, q_row;
+    long long k_batch, k_head, k_row;
+    long long v_batch, v_head, v_row;
+    long long out_batch, out_head, out_row;
+} la_window_strides;
+
+/*
+ * la_window_prefill -- a prompt, or a further piece of one.
+ *
+ *   q [B,Hq,N,d], k [B,Hkv,N,d], v [B,Hkv,N,dv], out [B,Hq,N,dv].
+ *   k_cache, v_cache  both or neither.  With them the new tokens follow the
+ *              pos[b] cached ones, and the call leaves the cache holding the
+ *              sinks and the last `window` other tokens (in place).  Without
+ *              them the sequences start at position 0 and pos must be NULL.
+ *   pos        NULL with a cache: every sequence starts empty.
+ *   seq_lens   HOST array of B lengths of a right-padded batch (0 <= seq_lens[b]
+ *              <= N), or NULL.  Padding rows never reach a result, whatever
+ *              they hold; padding rows of out are not written.
+ *   cfg        dtype and stream are used.
+ *
+ * Inside a sequence, values of v are expected to be finite: a token that a
+ * query does not see enters its sum with weight zero.
+ * LA_ERR_INVALID, LA_ERR_UNSUPPORTED, LA_ERR_ALIGN as elsewhere; LA_ERR_INVALID
+ * too if out, or a cache, overlaps k or v.
+ */
+LA_API la_status la_window_prefill(const void* q, const void* k, const void* v, void* out,
+                                   void* k_cache, void* v_cache, const int* pos, const int* seq_lens,
+                                   int B, int Hq, int Hkv, int N, int d, int dv, int window, int sinks, float scale,
+                                   const la_window_strides* strides, const la_config* cfg);
+
+/*
+ * la_window_decode_step -- one token of each sequence: writes its key and
+ * value into the cache's slot of position pos[b] and attends over the cache.
+ *
+ *   q [B,Hq,d], k [B,Hkv,d], v [B,Hkv,dv], out [B,Hq,dv]; caches and pos
+ *   (required) as above.  One kernel, no workspace.
+ */
+LA_API la_status la_window_decode_step(const void* q, const void* k, const void* v, void* out,
+                                       void* k_cache, void* v_cache, const int* pos,
+                                       int B, int Hq, int Hkv, int d, int dv, int window, int sinks, float scale,
+                                       const la_window_strides* strides, const la_config* cfg);
+
+/*
  * la_set_stage_events -- profiling hook, off by default.  With n > 0, every
  * later la_prefill / la_decode_step / la_gated_delta_decode_step /
- * la_causal_conv / la_ssm_conv / la_ssm_scan / la_ssm_step records
+ * la_causal_conv / la_ssm_conv / la_ssm_scan / la_ssm_step /
+ * la_window_prefill / la_window_decode_step records
  * events[i] on its cfg->stream right after launching its i-th kernel
  * (i < n; a call launches 1 to 16 kernels, la_prefill_kernel_count gives the
  * number for a prefill: bf16 LA_PLAIN/LA_DECAY prefill = segment summaries,
