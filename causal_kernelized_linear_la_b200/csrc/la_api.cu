@@ -262,7 +262,10 @@ la_status check_window(WindowArgs* w, const void* q, const void* k, const void* 
     if (!cfg || B < 0 || Hq < 0 || Hkv < 0 || N < 0 || window < 1 || sinks < 0) return LA_ERR_INVALID;
     if (cfg->dtype != LA_F32 && cfg->dtype != LA_BF16) return LA_ERR_INVALID;
     if (!head_ok(d) || !head_ok(dv)) return LA_ERR_UNSUPPORTED;
-    if ((long long)window + sinks > 0x7fffffffLL) return LA_ERR_INVALID;
+    constexpr int kTop = (1 << 30) - 1;   // row and slot numbers add up inside 32 bits
+    if (N > kTop || (k_cache && (long long)window + sinks > kTop)) return LA_ERR_UNSUPPORTED;
+    if (window > kTop) window = kTop;     // without a cache: more than any prompt reaches back
+    if (sinks > kTop) sinks = kTop;
     if (Hq > 0 && (Hkv == 0 || Hq % Hkv != 0)) return LA_ERR_INVALID;
     if (Hq > 65535) return LA_ERR_UNSUPPORTED;
     if (!(scale == scale) || scale - scale != 0.f) return LA_ERR_INVALID;   // NaN or infinite
@@ -283,6 +286,8 @@ la_status check_window(WindowArgs* w, const void* q, const void* k, const void* 
     for (const void* p : ptrs)
         if (!aligned16(p)) return LA_ERR_ALIGN;
     if (!aligned_to(pos, sizeof(int))) return LA_ERR_ALIGN;
+    // rows of one head do not share memory
+    if (N > 1 && (s.q_row < d || s.k_row < d || s.v_row < dv || s.out_row < dv)) return LA_ERR_INVALID;
     if (work > 0) {
         const size_t cap = (size_t)window + sinks;
         const size_t ks = extent4(B, Hkv, N, d, s.k_batch, s.k_head, s.k_row, e);
@@ -681,7 +686,8 @@ la_status la_window_prefill(const void* q, const void* k, const void* v, void* o
     const int step = la::launch_group(seq_lens);
     for (int b0 = 0; b0 < B; b0 += step) {
         const la::WindowArgs a = la::window_from(all, b0, B - b0 < step ? B - b0 : step);
-        cudaError_t err = la::launch_window_prefill_simt(a);
+        // bf16 prompts run on the tensor cores; fp32 inputs keep fp32 arithmetic
+        cudaError_t err = a.dtype == LA_BF16 ? la::launch_window_prefill_tc(a) : la::launch_window_prefill_simt(a);
         if (err == cudaSuccess) la::stage_mark(0, a.stream);
         if (err == cudaSuccess && a.k_cache) {
             err = la::launch_window_cache_update(a);
@@ -735,8 +741,9 @@ la_status la_prefill_check(const void* workspace, void* stream)
     const unsigned int e2 = la::read_and_clear_device_error_gdelta(s);
     const unsigned int e3 = la::read_and_clear_device_error_selftest(s);
     const unsigned int e4 = la::read_and_clear_device_error_gla(s);
+    const unsigned int e5 = la::read_and_clear_device_error_window(s);
     if (e1 == 4u || e2 == 4u || e4 == 4u) return LA_ERR_UNSUPPORTED;
-    if (e1 != 0 || e2 != 0 || e3 != 0 || e4 != 0) return LA_ERR_TIMEOUT;
+    if (e1 != 0 || e2 != 0 || e3 != 0 || e4 != 0 || e5 != 0) return LA_ERR_TIMEOUT;
     return LA_OK;
 }
 

@@ -36,6 +36,8 @@ struct WindowLens {
 };
 
 cudaError_t launch_window_prefill_simt(const WindowArgs& a);
+cudaError_t launch_window_prefill_tc(const WindowArgs& a);
+unsigned int read_and_clear_device_error_window(cudaStream_t stream);
 cudaError_t launch_window_cache_update(const WindowArgs& a);
 cudaError_t launch_window_decode(const WindowArgs& a);
 
@@ -114,6 +116,57 @@ struct KeyWalk {
     __device__ __forceinline__ bool sees_new(int i, int j) const
     {
         return j <= i && j < len && (i - j < window || j < sinks - start);
+    }
+
+    // The slots that query i sees, as three intervals of slot numbers: sinks,
+    // ring tokens written in the ring's current turn, ring tokens of the turn
+    // before.  (ring_age(r) > i - window solved for r on each side of `last`.)
+    struct Span {
+        int lo, hi;
+    };
+    __device__ __forceinline__ Span sink_slots() const { return {0, start < sinks ? start : sinks}; }
+    __device__ __forceinline__ Span turn_slots(int i) const
+    {
+        const int lo = i - window + last + 2;
+        return {sinks + (lo > 0 ? lo : 0), taken > 0 ? sinks + last + 1 : 0};
+    }
+    __device__ __forceinline__ Span past_slots(int i) const
+    {
+        const int lo = i + last + 2;
+        return {sinks + (lo > last + 1 ? lo : last + 1), sinks + (taken < window ? taken : window)};
+    }
+    __device__ __forceinline__ int sinks_left() const { return start < sinks ? sinks - start : 0; }
+
+    // some key of tile it is visible to some query of [qa, qb)
+    __device__ __forceinline__ bool any(int it, int qa, int qb) const
+    {
+        const int b = base(it);
+        if (!is_cache(it)) return b < qb && (b + T > qa - window + 1 || b < sinks_left());
+        const Span s = sink_slots(), t = turn_slots(qa), p = past_slots(qa);   // the first query sees the most
+        return b < s.hi || max(t.lo, b) < min(t.hi, b + T) || max(p.lo, b) < min(p.hi, b + T);
+    }
+    // every key of tile it is visible to every query of [qa, qb)
+    __device__ __forceinline__ bool all(int it, int qa, int qb) const
+    {
+        const int b = base(it), e = b + T;
+        if (!is_cache(it)) return e - 1 <= qa && e <= len && (b >= qb - window || e <= sinks_left());
+        const Span t = turn_slots(qb - 1), p = past_slots(qb - 1);             // the last query sees the least
+        return e <= sink_slots().hi || (b >= t.lo && e <= t.hi) || (b >= p.lo && e <= p.hi);
+    }
+    // keys of tile it, counted from its base, that hold a token: the rest may hold anything
+    __device__ __forceinline__ int live(int it) const
+    {
+        const int held = start < sinks ? start : sinks + (taken < window ? taken : window);
+        return (is_cache(it) ? held : len) - base(it);
+    }
+    // 32 keys from `key` on (a slot or a new token): bit c is set if query i sees key + c
+    __device__ __forceinline__ static uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+    __device__ __forceinline__ static uint32_t within(Span s, int key) { return below(s.hi - key) & ~below(s.lo - key); }
+    __device__ __forceinline__ uint32_t bits(bool old, int i, int key) const
+    {
+        if (old) return within(sink_slots(), key) | within(turn_slots(i), key) | within(past_slots(i), key);
+        const int end = i < len ? i + 1 : len;
+        return within({i - window + 1, end}, key) | within({0, min(end, sinks_left())}, key);
     }
 };
 

@@ -415,8 +415,9 @@ LA_API la_status la_ssm_step(const void* x, const void* delta, const float* A, c
  * The calls do not change pos, and slots not yet filled never reach a result.
  *
  * Query head h reads kv head h / (Hq / Hkv); Hq is a multiple of Hkv.  d, dv in
- * {64, 128}; window >= 1, sinks >= 0, sinks + window < 2^31; positions stay
- * below 2^31.  Sums, maxima and outputs accumulate in fp32.  All pointers are
+ * {64, 128}; window >= 1, sinks >= 0; N < 2^30 and, with a cache, sinks +
+ * window < 2^30 (LA_ERR_UNSUPPORTED); positions stay below 2^31; rows of one
+ * head are at least d (dv) elements apart.  Sums, maxima and outputs accumulate in fp32.  All pointers are
  * 16-byte aligned, and so are the rows (strides are multiples of 16 bytes).
  */
 
