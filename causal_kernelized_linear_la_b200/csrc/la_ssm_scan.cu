@@ -5,12 +5,15 @@
 // B and C are shared by the channels of a group.  States, step sizes, decays
 // and sums are fp32; y is rounded to the storage type once.
 //
-// Prompt scan.  A CTA walks the tokens of 32 channels in tiles of kTile.  Four
-// lanes share a channel, each with NS states in registers; the raw rows of
-// the tile after this one arrive by cp.async while this one is computed.  Per
-// tile the CTA first turns delta and x into (dt, dt x) and B, C into fp32, then
-// runs the recurrence, then finishes y: the softplus, the gate and the type
-// conversions are done once a value, not once a lane.
+// Prompt scan.  A CTA walks the tokens of a few channels in tiles of 16 or 32.
+// LANES lanes share a channel, each with NS states in registers, and do nothing
+// but the recurrence: per token and pair of states two products, two
+// exponentials and two FMAs as packed fp32 pairs, and one partial sum of y.
+// Other warps keep them fed and carry their results away: four bring the raw
+// rows by cp.async some tiles ahead and put (dt, dt x) and fp32 B, C of the
+// next tile into shared memory, four take y of the tile before out of it (the
+// lanes' partial sums, skip, gate), so softplus, gate and conversions are done
+// once a value, off the recurrence's path.
 // The decay needs one exponential per (token, channel, state): the SFU's 16 a
 // clock and SM bound the scan (at n = 16 its 2^x alone take three times as
 // long as reading delta, x, z and writing y), not memory.
@@ -28,11 +31,11 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kCh = 32;        // channels of a CTA
-constexpr int kLanes = 4;      // lanes sharing a channel
-constexpr int kThreads = kCh * kLanes;
-constexpr int kTile = 32;      // tokens of a tile
-constexpr int kYPitch = 40;    // fp32 row pitch of the y tile: four tokens x eight channels hit 32 banks
+constexpr int kRec = 128;      // threads of the recurrence
+constexpr int kPrep = 128;     // threads that load and prepare
+constexpr int kFin = 128;      // threads that finish y
+constexpr int kThreads = kRec + kPrep + kFin;
+constexpr int kRaw = 6;        // tiles of raw rows: up to three in use (prepared, in the recurrence, finished), the others in flight
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Lens {
@@ -67,230 +70,438 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
     return r;
 }
 
-__device__ __forceinline__ float softplus(float v) { return v > 20.f ? v : log1pf(expf(v)); }
+// log(1 + e^v) = max(v, 0) + log1p(e), e = e^-|v| in (0, 1], and log1p(e) =
+// 2 atanh(r) with r = e / (2 + e) <= 1/3: the odd series of atanh to r^13 is
+// off by r^14 / 15 < 2e-8 relative.
+__device__ __forceinline__ float softplus(float v)
+{
+    const float e = ex2_approx(-fabsf(v) * kLog2e);
+    const float r = __fdividef(e, 2.f + e), q = r * r;
+    float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
+    p = fmaf(p, q, 1.f / 9.f);
+    p = fmaf(p, q, 1.f / 7.f);
+    p = fmaf(p, q, 1.f / 5.f);
+    p = fmaf(p, q, 1.f / 3.f);
+    p = fmaf(p, q, 1.f);
+    return fmaf(2.f * r, p, fmaxf(v, 0.f));
+}
 template <typename T> __device__ __forceinline__ float silu(float v);
 template <> __device__ __forceinline__ float silu<float>(float v) { return v / (1.f + expf(-v)); }
 template <> __device__ __forceinline__ float silu<__nv_bfloat16>(float v) { return __fdividef(v, 1.f + __expf(-v)); }
 
-template <int BYTES>
-__device__ __forceinline__ void cp_async_n(void* dst, const void* src, uint32_t src_bytes)
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, uint32_t src_bytes)
 {
-    if (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(src_bytes)
-                     : "memory");
-    else
-        cp_async4(dst, src, src_bytes);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(src_bytes)
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t id, uint32_t count)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
-// A tile of `rows` (of kTile) x `cols` (of PITCH) elements of a row-major
-// tensor into shared memory, zeros elsewhere, in pieces of `piece` bytes (16,
-// 4, or the element itself where rows do not start on 4 bytes).
-template <typename T>
-__device__ __forceinline__ void load_tile(T* dst, const T* src, long long row_stride, int rows, int cols, int pitch,
-                                          int piece)
+// A tile of `rows` (of ROWS) x `cols` (of PITCH) elements of a row-major
+// tensor into shared memory, zeros elsewhere, in pieces of BYTES (4, or the
+// element itself), by the preparing threads: rows that do not start on 16 bytes.
+template <typename T, int ROWS, int PITCH, int BYTES>
+__device__ __forceinline__ void load_pieces(T* dst, const T* src, long long row_stride, int rows, int cols, int tid)
 {
-    const int per = piece / (int)sizeof(T);   // elements of a piece
-    const int n = pitch / per;
-    for (int e = threadIdx.x; e < kTile * n; e += kThreads) {
-        const int t = e / n, c = (e % n) * per;
-        const int left = t < rows ? min(per, max(0, cols - c)) : 0;
+    constexpr int PER = BYTES / (int)sizeof(T), N = PITCH / PER;
+#pragma unroll 4
+    for (int e = tid; e < ROWS * N; e += kPrep) {
+        const int t = e / N, c = (e % N) * PER;
+        const int left = t < rows ? min(PER, max(0, cols - c)) : 0;
         const T* s = left > 0 ? src + t * row_stride + c : src;
-        T* d = dst + t * pitch + c;
-        if (piece == 16) cp_async_n<16>(d, s, left * sizeof(T));
-        else if (piece == 4) cp_async_n<4>(d, s, left * sizeof(T));
+        T* d = dst + t * PITCH + c;
+        if (BYTES == 4) cp_async4(d, s, left * sizeof(T));
         else *d = left > 0 ? *s : from_f32<T>(0.f);
     }
 }
 
-template <typename T, int NS>
+template <int N> struct Int { static constexpr int value = N; };
+
+// Two neighbouring values (the first at an even place).
+template <typename T> __device__ __forceinline__ float2 load2(const T* p);
+template <> __device__ __forceinline__ float2 load2<float>(const float* p) { return *reinterpret_cast<const float2*>(p); }
+template <> __device__ __forceinline__ float2 load2<__nv_bfloat16>(const __nv_bfloat16* p)
+{
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+}
+__device__ __forceinline__ void store2(float* p, float a, float b) { *reinterpret_cast<float2*>(p) = make_float2(a, b); }
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b)
+{
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+}
+
+// Bytes of shared memory with tiles of tt tokens: the raw tiles, two prepared buffers.
+constexpr int plan_bytes(int esize, int ns, int lanes, int tt)
+{
+    const int ch = kRec / lanes, np = lanes * ns, bcp = np < 8 ? 8 : np;
+    return kRaw * tt * (3 * ch + 2 * bcp) * esize + 2 * tt * (ch * 8 + np * 8 + lanes * (ch + 8) * 4);
+}
+
+// LANES lanes share a channel, NS states each; tiles of TT tokens: 32 halve the
+// barriers a token costs, 16 where shared memory does not hold 32.
+template <typename T, int NS, int LANES>
 struct Plan {
-    static constexpr int NP = kLanes * NS;     // states, padded
-    static constexpr int BCP = NP < 8 ? 8 : NP;   // elements of a B or C row in shared memory: whole 16-byte pieces
-    static constexpr int ROW = kTile * kCh * (int)sizeof(T), BC = kTile * BCP * (int)sizeof(T);
-    // a stage: x, delta, z tiles, B, C tiles
-    static constexpr int STAGE = 3 * ROW + 2 * BC;
-    static constexpr int OFF_DU = 2 * STAGE;                    // (dt, dt, dt x, dt x) fp32 [kTile][kCh]
-    static constexpr int OFF_B = OFF_DU + kTile * kCh * 16;     // fp32 [kTile][NP]
-    static constexpr int OFF_C = OFF_B + kTile * NP * 4;
-    static constexpr int OFF_Y = OFF_C + kTile * NP * 4;        // fp32 [kTile][kYPitch]
-    static constexpr int BYTES = OFF_Y + kTile * kYPitch * 4;
+    static constexpr int TT = plan_bytes(sizeof(T), NS, LANES, 32) <= 232448 ? 32 : 16;
+    static constexpr int CH = kRec / LANES;        // channels of a CTA
+    static constexpr int NP = LANES * NS;          // states, padded
+    static constexpr int BCP = NP < 8 ? 8 : NP;    // elements of a raw B or C row: whole 16-byte pieces
+    static constexpr int ROW = TT * CH * (int)sizeof(T), BC = TT * BCP * (int)sizeof(T);
+    static constexpr int STAGE = 3 * ROW + 2 * BC; // raw x, delta, z, B, C
+    // partial sums of y: [TT][LANES][CH], 8 floats of padding a row put a warp's LANES rows on different banks
+    static constexpr int YP = CH + 8, YROW = LANES * YP;
+    // a buffer of prepared values: (dt, dt x) [TT][CH], (B.., C..) [TT][LANES][2 NS], y parts
+    static constexpr int DU = TT * CH * 8, BCF = TT * NP * 2 * 4, Y = TT * YROW * 4;
+    static constexpr int BUF = DU + BCF + Y;
+    static constexpr int OFF_BUF = kRaw * STAGE;
+    static constexpr int BYTES = OFF_BUF + 2 * BUF;
+    // 16-byte pieces of a raw row and of a tile
+    static constexpr int XP = CH * (int)sizeof(T) / 16, BP = BCP * (int)sizeof(T) / 16;
+    static constexpr int PIECES = TT * (3 * XP + 2 * BP), SLOTS = (PIECES + kPrep - 1) / kPrep;
 };
 
-// A segment's summary: end state [kCh][NP] from zero, then sum of dt [kCh].
-template <int NS> __host__ __device__ constexpr int slot_floats() { return kCh * (kLanes * NS + 1); }
+// Floats of a segment's summary: end states from zero [CH][NP], then sums of dt [CH].
+template <int NS, int LANES> __host__ __device__ constexpr int slot_floats() { return kRec / LANES * (LANES * NS + 1); }
+
+// Named barriers over the whole CTA; + buffer (tile & 1).
+//   kReady: the preparing threads (its values are in) and the finishing threads (its y parts are free) arrive,
+//           the recurrence waits
+//   kDone:  the recurrence arrives, the others wait
+enum Bars : uint32_t { kReady = 1, kDone = 3, kPrepBar = 5 };
 
 // grid: (channel tiles, segments, sequences).  SUMMARY: the first kernel of a
 // segmented scan; otherwise outputs and the final state.
-template <typename T, int NS, bool SUMMARY>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int NS, int LANES, bool SUMMARY>
+__global__ void __launch_bounds__(kThreads, 1)
 ssm_scan_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ Lens lens, int tiles_per_group, int px,
                 int pb)
 {
-    using P = Plan<T, NS>;
-    constexpr int NP = P::NP;
+    using P = Plan<T, NS, LANES>;
+    constexpr int NP = P::NP, CH = P::CH, TT = P::TT;
+    static_assert(P::BYTES <= 232448 && P::BYTES == plan_bytes(sizeof(T), NS, LANES, TT), "shared memory plan");
     extern __shared__ __align__(16) unsigned char sm[];
-    const int tid = threadIdx.x;
-    const int ch = tid / kLanes, l = tid % kLanes;     // a warp holds 8 channels x 4 lanes
     const int b = blockIdx.z, seg = blockIdx.y, tile = blockIdx.x;
     const int grp = tile / tiles_per_group, per = a.D / a.G;
-    const int cg0 = (tile % tiles_per_group) * kCh;    // first channel inside the group
-    const int c0 = grp * per + cg0, nch = min(kCh, per - cg0);
+    const int cg0 = (tile % tiles_per_group) * CH;     // first channel inside the group
+    const int c0 = grp * per + cg0, nch = min(CH, per - cg0);
     const int len = lens.use ? lens.n[b] : a.N;
     const int s0 = seg * a.seg_len, s1 = min(len, s0 + a.seg_len);
-    const bool mine = ch < nch;
-    const int c = c0 + (mine ? ch : 0);
+    const size_t unit0 = ((size_t)b * gridDim.x + tile) * a.segs;   // this chain's first summary slot
 
     if (SUMMARY) grid_launch_dependents();
     if (s0 >= len && !(seg == 0 && !SUMMARY)) return;   // an empty sequence still reports its start state
+    const int nt = s0 < s1 ? (s1 - s0 + TT - 1) / TT : 0;
 
-    // this lane's states and decay rates (in log2 units); padded states stay zero
-    f2 A2[(NS + 1) / 2], h[(NS + 1) / 2];
-#pragma unroll
-    for (int i = 0; i < NS; i += 2) {
-        const int s = l * NS + i;
-        const float* ap = a.A + (size_t)c * a.n;
-        A2[i / 2] = pack2(mine && s < a.n ? ap[s] * kLog2e : 0.f, NS > 1 && mine && s + 1 < a.n ? ap[s + 1] * kLog2e : 0.f);
-        const float* hp = a.h0 + ((size_t)b * a.D + c) * a.n;
-        const bool from = a.h0 && mine && seg == 0;
-        h[i / 2] = pack2(from && s < a.n ? hp[s] : 0.f, NS > 1 && from && s + 1 < a.n ? hp[s + 1] : 0.f);
-    }
-    const size_t unit0 = ((size_t)b * gridDim.x + tile) * a.segs;   // this chain's first summary slot
-    if (!SUMMARY && a.segs > 1) {
-        grid_dependency_wait();   // the summaries
-        for (int g = 0; g < seg; ++g) {
-            const float* slot = a.workspace + (unit0 + g) * slot_floats<NS>();
-            const float dt = slot[kCh * NP + ch];
-#pragma unroll
-            for (int i = 0; i < NS; i += 2) {
-                const float2 ar = unpack2(A2[i / 2]);
-                const float* e = slot + ch * NP + l * NS + i;
-                h[i / 2] = fma2(pack2(ex2_approx(dt * ar.x), ex2_approx(dt * ar.y)), h[i / 2],
-                                pack2(e[0], NS > 1 ? e[1] : 0.f));
-            }
-        }
-    }
-
-    const T* xp = (const T*)a.x + b * a.st.x_batch + c0;
-    const T* dp = (const T*)a.delta + b * a.st.delta_batch + c0;
-    const T* zp = a.z ? (const T*)a.z + b * a.st.z_batch + c0 : nullptr;
-    const T* bp = (const T*)a.Bm + b * a.st.B_batch + (size_t)grp * a.n;
-    const T* cp = (const T*)a.Cm + b * a.st.C_batch + (size_t)grp * a.n;
-    auto fetch = [&](int t, int stage) {
-        unsigned char* st = sm + stage * P::STAGE;
-        const int rows = s1 - t;
-        load_tile<T>((T*)st, xp + t * a.st.x_row, a.st.x_row, rows, nch, kCh, px);
-        load_tile<T>((T*)(st + P::ROW), dp + t * a.st.delta_row, a.st.delta_row, rows, nch, kCh, px);
-        if (!SUMMARY && zp) load_tile<T>((T*)(st + 2 * P::ROW), zp + t * a.st.z_row, a.st.z_row, rows, nch, kCh, px);
-        load_tile<T>((T*)(st + 3 * P::ROW), bp + t * a.st.B_row, a.st.B_row, rows, a.n, P::BCP, pb);
-        if (!SUMMARY) load_tile<T>((T*)(st + 3 * P::ROW + P::BC), cp + t * a.st.C_row, a.st.C_row, rows, a.n, P::BCP, pb);
-    };
-
-    float4* du = reinterpret_cast<float4*>(sm + P::OFF_DU);
-    float* Bf = reinterpret_cast<float*>(sm + P::OFF_B);
-    float* Cf = reinterpret_cast<float*>(sm + P::OFF_C);
-    float* yf = reinterpret_cast<float*>(sm + P::OFF_Y);
-    const int cc = tid % kCh, tr = tid / kCh;            // element-wise passes: channel and first token
-    const float bias = a.delta_bias && cc < nch ? a.delta_bias[c0 + cc] : 0.f;
-    const float skip = !SUMMARY && a.skip && cc < nch ? a.skip[c0 + cc] : 0.f;
-    float dt_sum = 0.f;                                   // of channel cc, over this thread's tokens
-
-    if (s0 < s1) fetch(s0, 0);
-    cp_async_commit();
-    int stage = 0;
-    for (int t0 = s0; t0 < s1; t0 += kTile, stage ^= 1) {
-        const int rows = min(kTile, s1 - t0);
-        cp_async_wait_all();
-        __syncthreads();   // this tile's rows are in, and the previous tile is done with
-        if (t0 + kTile < s1) fetch(t0 + kTile, stage ^ 1);
-        cp_async_commit();
-        const unsigned char* st = sm + stage * P::STAGE;
-        const T* xs = (const T*)st;
-        const T* ds = (const T*)(st + P::ROW);
-        const T* zs = (const T*)(st + 2 * P::ROW);
-        const T* bs = (const T*)(st + 3 * P::ROW);
-        const T* cs = (const T*)(st + 3 * P::ROW + P::BC);
-        for (int t = tr; t < kTile; t += kThreads / kCh) {
-            float dt = to_f32<T>(ds[t * kCh + cc]) + bias;
-            if (a.softplus) dt = softplus(dt);
-            if (t >= rows) dt = 0.f;                      // decay 1, nothing added
-            const float u = dt * to_f32<T>(xs[t * kCh + cc]);
-            du[t * kCh + cc] = make_float4(dt, dt, u, u);
-            if (SUMMARY) dt_sum += dt;
-        }
-        for (int e = tid; e < kTile * NP; e += kThreads) {
-            const int at = (e / NP) * P::BCP + e % NP;
-            Bf[e] = to_f32<T>(bs[at]);
-            if (!SUMMARY) Cf[e] = to_f32<T>(cs[at]);
-        }
-        __syncthreads();
-#pragma unroll 1
-        for (int t = 0; t < kTile; t += 4) {
-            float part[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const ulonglong2 d2 = reinterpret_cast<const ulonglong2*>(du)[(t + j) * kCh + ch];
-                f2 acc = 0;
-                if (NS == 1) {
-                    const float a1 = ex2_approx(unpack2(d2.x).x * unpack2(A2[0]).x);
-                    const float h1 = fmaf(a1, unpack2(h[0]).x, unpack2(d2.y).x * Bf[(t + j) * NP + l]);
-                    h[0] = pack2(h1, 0.f);
-                    if (!SUMMARY) acc = pack2(h1 * Cf[(t + j) * NP + l], 0.f);
-                } else {
-                    const f2* B2 = reinterpret_cast<const f2*>(Bf + (t + j) * NP + l * NS);
-                    const f2* C2 = reinterpret_cast<const f2*>(Cf + (t + j) * NP + l * NS);
-#pragma unroll
-                    for (int i = 0; i < NS / 2; ++i) {
-                        const float2 e = unpack2(mul2(d2.x, A2[i]));
-                        h[i] = fma2(pack2(ex2_approx(e.x), ex2_approx(e.y)), h[i], mul2(d2.y, B2[i]));
-                        if (!SUMMARY) acc = fma2(C2[i], h[i], acc);
-                    }
-                }
-                const float2 s = unpack2(acc);
-                part[j] = s.x + s.y;
-            }
-            if (!SUMMARY) {
-                // sum over the channel's four lanes; lane l ends with token t + l
-                const bool o2 = l & 2, o1 = l & 1;
-                const float k0 = (o2 ? part[2] : part[0]) + __shfl_xor_sync(~0u, o2 ? part[0] : part[2], 2);
-                const float k1 = (o2 ? part[3] : part[1]) + __shfl_xor_sync(~0u, o2 ? part[1] : part[3], 2);
-                yf[(t + l) * kYPitch + ch] = (o1 ? k1 : k0) + __shfl_xor_sync(~0u, o1 ? k0 : k1, 1);
-            }
-        }
-        if (!SUMMARY) {
-            __syncthreads();
-            T* yp = (T*)a.out + (size_t)b * a.N * a.D + c0 + cc;
-            if (cc < nch) {
-                for (int t = tr; t < rows; t += kThreads / kCh) {
-                    float y = fmaf(skip, to_f32<T>(xs[t * kCh + cc]), yf[t * kYPitch + cc]);
-                    if (zp) y *= silu<T>(to_f32<T>(zs[t * kCh + cc]));
-                    yp[(size_t)(t0 + t) * a.D] = from_f32<T>(y);
-                }
-            }
-        }
-    }
-
-    if (SUMMARY) {
-        // sum of dt over the four threads of each channel
-        __syncthreads();
-        yf[tr * kYPitch + cc] = dt_sum;
-        __syncthreads();
-        float* slot = a.workspace + (unit0 + seg) * slot_floats<NS>();
-        if (tid < kCh)
-            slot[kCh * NP + tid] = yf[tid] + yf[kYPitch + tid] + yf[2 * kYPitch + tid] + yf[3 * kYPitch + tid];
-#pragma unroll
-        for (int i = 0; i < NS; i += 2) {
-            const float2 v = unpack2(h[i / 2]);
-            slot[ch * NP + l * NS + i] = v.x;
-            if (NS > 1) slot[ch * NP + l * NS + i + 1] = v.y;
-        }
-    } else if (s1 == len && mine && a.h_out) {
-        float* hp = a.h_out + ((size_t)b * a.D + c) * a.n;
+    if (threadIdx.x < kRec) {
+        // ---------------- the recurrence ----------------
+        // neighbouring lanes are channels: the lanes that read one (B, C) piece sit side by side,
+        // which halves the shared-memory cycles of a 16-byte read (2 instead of 4, measured)
+        constexpr int WCH = 32 / LANES;    // channels of a warp
+        const int ch = threadIdx.x / 32 * WCH + threadIdx.x % WCH, l = threadIdx.x % 32 / WCH;
+        const bool mine = ch < nch;
+        const int c = c0 + (mine ? ch : 0);
+        // this lane's decay rates (in log2 units) and states; padded states stay zero
+        f2 A2[(NS + 1) / 2], h[(NS + 1) / 2];
 #pragma unroll
         for (int i = 0; i < NS; i += 2) {
             const int s = l * NS + i;
-            const float2 v = unpack2(h[i / 2]);
-            if (s < a.n) hp[s] = v.x;
-            if (NS > 1 && s + 1 < a.n) hp[s + 1] = v.y;
+            const float* ap = a.A + (size_t)c * a.n;
+            A2[i / 2] = pack2(mine && s < a.n ? ap[s] * kLog2e : 0.f,
+                              NS > 1 && mine && s + 1 < a.n ? ap[s + 1] * kLog2e : 0.f);
+            const float* hp = a.h0 + ((size_t)b * a.D + c) * a.n;
+            const bool from = a.h0 && mine && seg == 0;
+            h[i / 2] = pack2(from && s < a.n ? hp[s] : 0.f, NS > 1 && from && s + 1 < a.n ? hp[s + 1] : 0.f);
+        }
+        if (!SUMMARY && a.segs > 1) {
+            grid_dependency_wait();   // the summaries
+            for (int g = 0; g < seg; ++g) {
+                const float* slot = a.workspace + (unit0 + g) * slot_floats<NS, LANES>();
+                const float dt = slot[CH * NP + ch];
+#pragma unroll
+                for (int i = 0; i < NS; i += 2) {
+                    const float2 ar = unpack2(A2[i / 2]);
+                    const float* e = slot + ch * NP + l * NS + i;
+                    h[i / 2] = fma2(pack2(ex2_approx(dt * ar.x), ex2_approx(dt * ar.y)), h[i / 2],
+                                    pack2(e[0], NS > 1 ? e[1] : 0.f));
+                }
+            }
+        }
+        // Tokens go NB at a time: decays, written terms and C of the next NB are
+        // loaded and computed ahead of this NB's chain of FMAs, so that the
+        // exponentials (8 clocks each) and the chain overlap in one warp; the
+        // loads also come before the stores of y, above which none is moved.
+        constexpr int NB = NS <= 2 ? 8 : NS == 4 ? 4 : 2, NH = (NS + 1) / 2;
+        for (int k = 0; k < nt; ++k) {
+            unsigned char* buf = sm + P::OFF_BUF + (k & 1) * P::BUF;
+            const float2* du = reinterpret_cast<const float2*>(buf) + ch;
+            const float* bc = reinterpret_cast<const float*>(buf + P::DU) + l * 2 * NS;
+            float* yp = reinterpret_cast<float*>(buf + P::DU + P::BCF) + l * P::YP + ch;
+            f2 dec[2][NB][NH], add[2][NB][NH], cv[2][NB][NH];
+            auto take = [&](int t0, int w) {
+#pragma unroll
+                for (int t = 0; t < NB; ++t) {
+                    const float2 d = du[(t0 + t) * CH];
+                    const f2 dt = pack2(d.x, d.x), u = pack2(d.y, d.y);
+                    const float* q = bc + (t0 + t) * NP * 2;
+                    f2 bv[NH];
+                    if (NS == 1) {
+                        const float2 v = *reinterpret_cast<const float2*>(q);
+                        bv[0] = pack2(v.x, 0.f);
+                        cv[w][t][0] = pack2(v.y, 0.f);
+                    } else if (NS == 2) {
+                        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(q);
+                        bv[0] = v.x;
+                        cv[w][t][0] = v.y;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < NH; i += 2) {
+                            const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(q + 2 * i);
+                            const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(q + NS + 2 * i);
+                            bv[i] = v.x;
+                            bv[i + (NH > 1)] = v.y;
+                            cv[w][t][i] = x.x;
+                            cv[w][t][i + (NH > 1)] = x.y;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < NH; ++i) {
+                        const float2 e = unpack2(mul2(dt, A2[i]));
+                        dec[w][t][i] = pack2(ex2_approx(e.x), NS > 1 ? ex2_approx(e.y) : 0.f);
+                        add[w][t][i] = mul2(u, bv[i]);
+                    }
+                }
+            };
+            named_bar(kReady + (k & 1), kThreads);
+            take(0, 0);
+#pragma unroll
+            for (int t0 = 0; t0 < TT; t0 += NB) {
+                const int w = t0 / NB & 1;
+                if (t0 + NB < TT) take(t0 + NB, w ^ 1);
+#pragma unroll
+                for (int t = 0; t < NB; ++t) {
+                    f2 acc = 0;
+#pragma unroll
+                    for (int i = 0; i < NH; ++i) {
+                        h[i] = fma2(dec[w][t][i], h[i], add[w][t][i]);
+                        acc = i == 0 ? mul2(cv[w][t][i], h[i]) : fma2(cv[w][t][i], h[i], acc);
+                    }
+                    if (!SUMMARY) {
+                        const float2 q = unpack2(acc);
+                        yp[(t0 + t) * P::YROW] = q.x + q.y;
+                    }
+                }
+            }
+            bar_arrive(kDone + (k & 1), kThreads);
+        }
+        if (SUMMARY) {
+            float* slot = a.workspace + (unit0 + seg) * slot_floats<NS, LANES>();
+#pragma unroll
+            for (int i = 0; i < NS; i += 2) {
+                const float2 v = unpack2(h[i / 2]);
+                slot[ch * NP + l * NS + i] = v.x;
+                if (NS > 1) slot[ch * NP + l * NS + i + 1] = v.y;
+            }
+        } else if (s1 == len && mine && a.h_out) {
+            float* hp = a.h_out + ((size_t)b * a.D + c) * a.n;
+#pragma unroll
+            for (int i = 0; i < NS; i += 2) {
+                const int s = l * NS + i;
+                const float2 v = unpack2(h[i / 2]);
+                if (s < a.n) hp[s] = v.x;
+                if (NS > 1 && s + 1 < a.n) hp[s + 1] = v.y;
+            }
+        }
+    } else if (threadIdx.x < kRec + kPrep) {
+        // ---------------- load and prepare ----------------
+        const int tid = threadIdx.x - kRec;
+        const int cc = tid % (CH / 2) * 2, tr = tid / (CH / 2);   // this thread's channels cc, cc + 1 and first row
+        constexpr int TR = kPrep / (CH / 2);                      // rows a pass covers
+        const T* xp = (const T*)a.x + b * a.st.x_batch + s0 * a.st.x_row + c0;
+        const T* dp = (const T*)a.delta + b * a.st.delta_batch + s0 * a.st.delta_row + c0;
+        const T* zp = a.z ? (const T*)a.z + b * a.st.z_batch + s0 * a.st.z_row + c0 : nullptr;
+        const T* bp = (const T*)a.Bm + b * a.st.B_batch + s0 * a.st.B_row + (size_t)grp * a.n;
+        const T* cp = (const T*)a.Cm + b * a.st.C_batch + s0 * a.st.C_row + (size_t)grp * a.n;
+        float bias[2], dt_sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) bias[j] = a.delta_bias && cc + j < nch ? a.delta_bias[c0 + cc + j] : 0.f;
+
+        // this thread's 16-byte pieces of every tile, where all rows start on 16 bytes
+        const bool wide = px == 16 && pb == 16;
+        const char* src[P::SLOTS];
+        long long step[P::SLOTS];
+        int dst[P::SLOTS], rowof[P::SLOTS];      // rowof: the piece's token of the tile, past TT where there is nothing to read
+        uint32_t bytes[P::SLOTS];
+        if (wide) {
+#pragma unroll
+            for (int i = 0; i < P::SLOTS; ++i) {
+                const int e = tid + i * kPrep;
+                const bool is_x = e < TT * 3 * P::XP;
+                const int r = is_x ? e % (TT * P::XP) : (e - TT * 3 * P::XP) % (TT * P::BP);
+                const int which = is_x ? e / (TT * P::XP) : 3 + (e - TT * 3 * P::XP) / (TT * P::BP);
+                const int n16 = is_x ? P::XP : P::BP, t = r / n16, col = r % n16 * (16 / (int)sizeof(T));
+                const T* base = which == 0 ? xp : which == 1 ? dp : which == 2 ? zp : which == 3 ? bp : cp;
+                const long long row = which == 0 ? a.st.x_row : which == 1 ? a.st.delta_row : which == 2 ? a.st.z_row :
+                                      which == 3 ? a.st.B_row : a.st.C_row;
+                const int left = (is_x ? nch : a.n) - col;
+                const bool on = e < P::PIECES && left > 0 && base && !(SUMMARY && (which == 2 || which == 4));
+                src[i] = (const char*)(base ? base + t * row + col : xp);
+                step[i] = row * TT * (long long)sizeof(T);
+                dst[i] = (which < 3 ? which * P::ROW : 3 * P::ROW + (which - 3) * P::BC) + r * 16;
+                bytes[i] = on ? min(left * (int)sizeof(T), 16) : 0;
+                rowof[i] = on ? t : 0x3fffffff;
+                if (e >= P::PIECES) dst[i] = -1;
+            }
+        }
+        auto raw = [&](int k) { return sm + (k % kRaw) * P::STAGE; };
+        auto fetch = [&](int k) {
+            if (k < nt) {
+                unsigned char* st = raw(k);
+                const int rows = s1 - s0 - k * TT;
+                if (wide) {
+#pragma unroll
+                    for (int i = 0; i < P::SLOTS; ++i) {
+                        if (dst[i] >= 0) {
+                            const bool on = rowof[i] < rows;
+                            cp_async16(st + dst[i], on ? src[i] : (const char*)xp, on ? bytes[i] : 0);
+                        }
+                        src[i] += step[i];
+                    }
+                } else {
+                    const long long t = (long long)k * TT;
+                    auto narrow = [&](auto piece) {
+                        constexpr int BYTES = decltype(piece)::value;
+                        load_pieces<T, TT, CH, BYTES>((T*)st, xp + t * a.st.x_row, a.st.x_row, rows, nch, tid);
+                        load_pieces<T, TT, CH, BYTES>((T*)(st + P::ROW), dp + t * a.st.delta_row, a.st.delta_row, rows, nch, tid);
+                        if (!SUMMARY && zp)
+                            load_pieces<T, TT, CH, BYTES>((T*)(st + 2 * P::ROW), zp + t * a.st.z_row, a.st.z_row, rows, nch, tid);
+                        load_pieces<T, TT, P::BCP, BYTES>((T*)(st + 3 * P::ROW), bp + t * a.st.B_row, a.st.B_row, rows, a.n, tid);
+                        if (!SUMMARY)
+                            load_pieces<T, TT, P::BCP, BYTES>((T*)(st + 3 * P::ROW + P::BC), cp + t * a.st.C_row, a.st.C_row,
+                                                              rows, a.n, tid);
+                    };
+                    if (px >= 4 && pb >= 4) narrow(Int<4>{});
+                    else narrow(Int<(int)sizeof(T)>{});
+                }
+            }
+            cp_async_commit();
+        };
+        // (B.., C..) of one lane and token side by side
+        auto spread = [&](float* bc, const T* bs, const T* cs) {
+            if (NS == 1) {
+#pragma unroll
+                for (int e = tid; e < TT * NP; e += kPrep) {
+                    const int t = e / NP, s = e % NP;
+                    bc[e * 2] = to_f32<T>(bs[t * P::BCP + s]);
+                    if (!SUMMARY) bc[e * 2 + 1] = to_f32<T>(cs[t * P::BCP + s]);
+                }
+            } else {
+#pragma unroll
+                for (int e = tid; e < TT * NP / 2; e += kPrep) {
+                    const int t = e / (NP / 2), s = e % (NP / 2) * 2;
+                    float* to = bc + t * NP * 2 + s / NS * 2 * NS + s % NS;
+                    *reinterpret_cast<float2*>(to) = load2<T>(bs + t * P::BCP + s);
+                    if (!SUMMARY) *reinterpret_cast<float2*>(to + NS) = load2<T>(cs + t * P::BCP + s);
+                }
+            }
+        };
+#pragma unroll
+        for (int k = 0; k < kRaw - 3; ++k) fetch(k);
+        for (int k = 0; k < nt; ++k) {
+            // tile k - 2 is through the recurrence (its buffer is free) and tile k - 3 is finished (its raw rows are free)
+            if (k >= 2) named_bar(kDone + (k & 1), kThreads);
+            cp_async_wait<kRaw - 4>();
+            named_bar(kPrepBar, kPrep);               // tile k is in shared memory for every preparing thread
+            const unsigned char* st = raw(k);
+            unsigned char* buf = sm + P::OFF_BUF + (k & 1) * P::BUF;
+            const T* xs = (const T*)st;
+            const T* ds = (const T*)(st + P::ROW);
+            float2* du = reinterpret_cast<float2*>(buf);
+            const int rows = s1 - s0 - k * TT;
+            spread(reinterpret_cast<float*>(buf + P::DU), (const T*)(st + 3 * P::ROW), (const T*)(st + 3 * P::ROW + P::BC));
+#pragma unroll
+            for (int i = 0; i < TT / TR; ++i) {
+                const int t = tr + i * TR;
+                const float2 d2 = load2<T>(ds + t * CH + cc), x2 = load2<T>(xs + t * CH + cc);
+                float dt[2] = {d2.x + bias[0], d2.y + bias[1]};
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (a.softplus) dt[j] = softplus(dt[j]);
+                    if (t >= rows) dt[j] = 0.f;           // decay 1, nothing added
+                    if (SUMMARY) dt_sum[j] += dt[j];
+                }
+                *reinterpret_cast<float4*>(du + t * CH + cc) = make_float4(dt[0], dt[0] * x2.x, dt[1], dt[1] * x2.y);
+            }
+            bar_arrive(kReady + (k & 1), kThreads);
+            fetch(k + kRaw - 3);                          // into the rows of tile k - 3
+        }
+        // the barriers that the other threads still pass
+        for (int k = max(nt, 2); k < nt + 2; ++k) named_bar(kDone + (k & 1), kThreads);
+        if (SUMMARY) {
+            // sum of dt over the threads of each channel
+            named_bar(kPrepBar, kPrep);
+            float* part = reinterpret_cast<float*>(sm);
+            part[tr * CH + cc] = dt_sum[0];
+            part[tr * CH + cc + 1] = dt_sum[1];
+            named_bar(kPrepBar, kPrep);
+            if (tid < CH) {
+                float sum = 0.f;
+                for (int i = 0; i < TR; ++i) sum += part[i * CH + tid];
+                a.workspace[(unit0 + seg) * slot_floats<NS, LANES>() + CH * NP + tid] = sum;
+            }
+        }
+    } else {
+        // ---------------- finish y ----------------
+        const int tid = threadIdx.x - kRec - kPrep;
+        const int cc = tid % (CH / 2) * 2, tr = tid / (CH / 2);
+        constexpr int TR = kFin / (CH / 2);
+        float skip[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) skip[j] = !SUMMARY && a.skip && cc + j < nch ? a.skip[c0 + cc + j] : 0.f;
+        // rows of out that take two values in one store
+        const bool pairs = a.D % 2 == 0 && c0 % 2 == 0 && nch % 2 == 0 && reinterpret_cast<uintptr_t>(a.out) % (2 * sizeof(T)) == 0;
+        T* op = (T*)a.out + ((size_t)b * a.N + s0) * a.D + c0 + cc;
+        for (int k = 0; k < min(nt, 2); ++k) bar_arrive(kReady + k, kThreads);     // the y parts are free
+        for (int k = 0; k < nt; ++k) {
+            named_bar(kDone + (k & 1), kThreads);
+            if (!SUMMARY) {
+                const unsigned char* st = sm + (k % kRaw) * P::STAGE;
+                const float* yp = reinterpret_cast<const float*>(sm + P::OFF_BUF + (k & 1) * P::BUF + P::DU + P::BCF) + cc;
+                const T* xs = (const T*)st;
+                const T* zs = (const T*)(st + 2 * P::ROW);
+                const int rows = s1 - s0 - k * TT;
+#pragma unroll 4
+                for (int i = 0; i < TT / TR; ++i) {
+                    const int t = tr + i * TR;
+                    const float2 x2 = load2<T>(xs + t * CH + cc);
+                    float y[2] = {0.f, 0.f};
+#pragma unroll
+                    for (int j = 0; j < LANES; ++j) {
+                        const float2 p = *reinterpret_cast<const float2*>(yp + t * P::YROW + j * P::YP);
+                        y[0] += p.x;
+                        y[1] += p.y;
+                    }
+                    y[0] = fmaf(skip[0], x2.x, y[0]);
+                    y[1] = fmaf(skip[1], x2.y, y[1]);
+                    if (a.z) {
+                        const float2 z2 = load2<T>(zs + t * CH + cc);
+                        y[0] *= silu<T>(z2.x);
+                        y[1] *= silu<T>(z2.y);
+                    }
+                    T* o = op + (size_t)(k * TT + t) * a.D;
+                    if (t < rows && pairs && cc < nch) store2(o, y[0], y[1]);
+                    else if (t < rows) {
+                        if (cc < nch) o[0] = from_f32<T>(y[0]);
+                        if (cc + 1 < nch) o[1] = from_f32<T>(y[1]);
+                    }
+                }
+            }
+            if (k + 2 < nt) bar_arrive(kReady + (k & 1), kThreads);
         }
     }
 }
@@ -302,12 +513,12 @@ int piece_of(const void* p, long long batch, long long row, int e)
     return m % 16 == 0 ? 16 : m % 4 == 0 ? 4 : e;
 }
 
-template <typename T, int NS>
+template <typename T, int NS, int LANES>
 cudaError_t launch_scan_ns(const SsmArgs& a)
 {
-    using P = Plan<T, NS>;
+    using P = Plan<T, NS, LANES>;
     const int e = sizeof(T);
-    const int per = a.D / a.G, tpg = (per + kCh - 1) / kCh;
+    const int per = a.D / a.G, tpg = (per + P::CH - 1) / P::CH;
     Lens lens{};
     lens.use = a.seq_lens != nullptr;
     if (a.seq_lens)
@@ -321,8 +532,8 @@ cudaError_t launch_scan_ns(const SsmArgs& a)
     int pb = piece_of(a.Bm, a.st.B_batch, a.st.B_row, e);
     pb = min(pb, piece_of(a.Cm, a.st.C_batch, a.st.C_row, e));
     pb = min(pb, piece_of(nullptr, noff, 0, e));
-    auto main_k = ssm_scan_kernel<T, NS, false>;
-    auto sum_k = ssm_scan_kernel<T, NS, true>;
+    auto main_k = ssm_scan_kernel<T, NS, LANES, false>;
+    auto sum_k = ssm_scan_kernel<T, NS, LANES, true>;
     cudaError_t err = cudaFuncSetAttribute(main_k, cudaFuncAttributeMaxDynamicSharedMemorySize, P::BYTES);
     if (err == cudaSuccess) err = cudaFuncSetAttribute(sum_k, cudaFuncAttributeMaxDynamicSharedMemorySize, P::BYTES);
     if (err != cudaSuccess) return err;
@@ -347,32 +558,30 @@ cudaError_t launch_scan_ns(const SsmArgs& a)
     return err;
 }
 
+// Lanes a channel: four, eight where sixteen states a lane would not fit its registers.
+int lanes_for(int n) { return n > 32 ? 8 : 4; }
+
 template <typename T>
 cudaError_t launch_scan_t(const SsmArgs& a)
 {
-    if (a.n <= 4) return launch_scan_ns<T, 1>(a);
-    if (a.n <= 8) return launch_scan_ns<T, 2>(a);
-    if (a.n <= 16) return launch_scan_ns<T, 4>(a);
-    if (a.n <= 32) return launch_scan_ns<T, 8>(a);
-    return launch_scan_ns<T, 16>(a);
+    if (a.n <= 4) return launch_scan_ns<T, 1, 4>(a);
+    if (a.n <= 8) return launch_scan_ns<T, 2, 4>(a);
+    if (a.n <= 16) return launch_scan_ns<T, 4, 4>(a);
+    if (a.n <= 32) return launch_scan_ns<T, 8, 4>(a);
+    return launch_scan_ns<T, 8, 8>(a);
 }
 
 }  // namespace
 
 void ssm_scan_segments(int B, int N, int D, int G, int n, int* segs, int* seg_len)
 {
-    (void)n;
-    const int per = D / G;
-    const long long units = (long long)B * G * ((per + kCh - 1) / kCh);
-    // enough CTAs for every SM sub-partition to hold a warp or two; segments stay long enough to pay for their summary
+    const int ch = kRec / lanes_for(n);
+    const long long units = (long long)B * G * ((D / G + ch - 1) / ch);
     int g = 1;
-    if (units < 96) {
-        const int want = (int)((256 + units - 1) / units);
-        const int most = N / 256;
-        g = max(1, min(min(want, most), 64));
-    }
-    const int L = ((N + g - 1) / g + kTile - 1) / kTile * kTile;
-    *seg_len = L > 0 ? L : kTile;
+    // a segment more than one costs a second pass over the exponentials
+    if (units < 60) g = (int)max(1ll, min(min(148 / units, (long long)N / 128), 64ll));
+    const int L = ((N + g - 1) / g + 31) / 32 * 32;   // whole tiles
+    *seg_len = L > 0 ? L : 32;
     *segs = N > 0 ? (N + *seg_len - 1) / *seg_len : 1;
 }
 
@@ -382,8 +591,8 @@ size_t ssm_scan_workspace_bytes(int B, int N, int D, int G, int n)
     ssm_scan_segments(B, N, D, G, n, &segs, &len);
     if (segs <= 1) return 0;
     const int np = n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 64;
-    const int per = D / G;
-    return (size_t)B * G * ((per + kCh - 1) / kCh) * segs * kCh * (np + 1) * sizeof(float);
+    const int ch = kRec / lanes_for(n);
+    return (size_t)B * G * ((D / G + ch - 1) / ch) * segs * ch * (np + 1) * sizeof(float);
 }
 
 cudaError_t launch_ssm_scan(const SsmArgs& a)
