@@ -31,11 +31,11 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kRec = 128;      // threads of the recurrence
+constexpr int kCh = 32;        // channels of a CTA; LANES lanes share one
 constexpr int kPrep = 128;     // threads that load and prepare
 constexpr int kFin = 128;      // threads that finish y
-constexpr int kThreads = kRec + kPrep + kFin;
-constexpr int kRaw = 6;        // tiles of raw rows: up to three in use (prepared, in the recurrence, finished), the others in flight
+constexpr int kBufs = 3;       // prepared tiles: one in the recurrence, one being finished, one being prepared
+constexpr int kRaw = kBufs + 4;   // tiles of raw rows: those of the prepared tiles and one being prepared, the others in flight
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Lens {
@@ -140,8 +140,8 @@ __device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b)
 // Bytes of shared memory with tiles of tt tokens: the raw tiles, two prepared buffers.
 constexpr int plan_bytes(int esize, int ns, int lanes, int tt)
 {
-    const int ch = kRec / lanes, np = lanes * ns, bcp = np < 8 ? 8 : np;
-    return kRaw * tt * (3 * ch + 2 * bcp) * esize + 2 * tt * (ch * 8 + np * 8 + lanes * (ch + 8) * 4);
+    const int ch = kCh, np = lanes * ns, bcp = np < 8 ? 8 : np;
+    return kRaw * tt * (3 * ch + 2 * bcp) * esize + kBufs * tt * (ch * 8 + np * 8 + lanes * (ch + 8) * 4);
 }
 
 // LANES lanes share a channel, NS states each; tiles of TT tokens: 32 halve the
@@ -149,7 +149,8 @@ constexpr int plan_bytes(int esize, int ns, int lanes, int tt)
 template <typename T, int NS, int LANES>
 struct Plan {
     static constexpr int TT = plan_bytes(sizeof(T), NS, LANES, 32) <= 232448 ? 32 : 16;
-    static constexpr int CH = kRec / LANES;        // channels of a CTA
+    static constexpr int CH = kCh;
+    static constexpr int REC = kCh * LANES, THREADS = REC + kPrep + kFin;   // threads of the recurrence, of the CTA
     static constexpr int NP = LANES * NS;          // states, padded
     static constexpr int BCP = NP < 8 ? 8 : NP;    // elements of a raw B or C row: whole 16-byte pieces
     static constexpr int ROW = TT * CH * (int)sizeof(T), BC = TT * BCP * (int)sizeof(T);
@@ -160,30 +161,30 @@ struct Plan {
     static constexpr int DU = TT * CH * 8, BCF = TT * NP * 2 * 4, Y = TT * YROW * 4;
     static constexpr int BUF = DU + BCF + Y;
     static constexpr int OFF_BUF = kRaw * STAGE;
-    static constexpr int BYTES = OFF_BUF + 2 * BUF;
+    static constexpr int BYTES = OFF_BUF + kBufs * BUF;
     // 16-byte pieces of a raw row and of a tile
     static constexpr int XP = CH * (int)sizeof(T) / 16, BP = BCP * (int)sizeof(T) / 16;
     static constexpr int PIECES = TT * (3 * XP + 2 * BP), SLOTS = (PIECES + kPrep - 1) / kPrep;
 };
 
 // Floats of a segment's summary: end states from zero [CH][NP], then sums of dt [CH].
-template <int NS, int LANES> __host__ __device__ constexpr int slot_floats() { return kRec / LANES * (LANES * NS + 1); }
+template <int NS, int LANES> __host__ __device__ constexpr int slot_floats() { return kCh * (LANES * NS + 1); }
 
-// Named barriers over the whole CTA; + buffer (tile & 1).
+// Named barriers over the whole CTA; + buffer (tile % kBufs).
 //   kReady: the preparing threads (its values are in) and the finishing threads (its y parts are free) arrive,
 //           the recurrence waits
 //   kDone:  the recurrence arrives, the others wait
-enum Bars : uint32_t { kReady = 1, kDone = 3, kPrepBar = 5 };
+enum Bars : uint32_t { kReady = 1, kDone = kReady + kBufs, kPrepBar = kDone + kBufs };
 
 // grid: (channel tiles, segments, sequences).  SUMMARY: the first kernel of a
 // segmented scan; otherwise outputs and the final state.
 template <typename T, int NS, int LANES, bool SUMMARY>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Plan<T, NS, LANES>::THREADS, 1)
 ssm_scan_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ Lens lens, int tiles_per_group, int px,
                 int pb)
 {
     using P = Plan<T, NS, LANES>;
-    constexpr int NP = P::NP, CH = P::CH, TT = P::TT;
+    constexpr int NP = P::NP, CH = P::CH, TT = P::TT, kRec = P::REC, kThreads = P::THREADS;
     static_assert(P::BYTES <= 232448 && P::BYTES == plan_bytes(sizeof(T), NS, LANES, TT), "shared memory plan");
     extern __shared__ __align__(16) unsigned char sm[];
     const int b = blockIdx.z, seg = blockIdx.y, tile = blockIdx.x;
@@ -236,68 +237,74 @@ ssm_scan_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ Lens 
         // loaded and computed ahead of this NB's chain of FMAs, so that the
         // exponentials (8 clocks each) and the chain overlap in one warp; the
         // loads also come before the stores of y, above which none is moved.
-        constexpr int NB = NS <= 2 ? 8 : NS == 4 ? 4 : 2, NH = (NS + 1) / 2;
-        for (int k = 0; k < nt; ++k) {
-            unsigned char* buf = sm + P::OFF_BUF + (k & 1) * P::BUF;
+        constexpr int NB = NS <= 2 ? 4 : NS == 4 ? 4 : 2, NH = (NS + 1) / 2;
+        float2 dv[2][NB];                               // (dt, dt x)
+        f2 dec[2][NB][NH], bv[2][NB][NH], cv[2][NB][NH];
+        auto load = [&](int k, int t0, int w) {
+            const unsigned char* buf = sm + P::OFF_BUF + (k % kBufs) * P::BUF;
             const float2* du = reinterpret_cast<const float2*>(buf) + ch;
             const float* bc = reinterpret_cast<const float*>(buf + P::DU) + l * 2 * NS;
-            float* yp = reinterpret_cast<float*>(buf + P::DU + P::BCF) + l * P::YP + ch;
-            f2 dec[2][NB][NH], add[2][NB][NH], cv[2][NB][NH];
-            auto take = [&](int t0, int w) {
 #pragma unroll
-                for (int t = 0; t < NB; ++t) {
-                    const float2 d = du[(t0 + t) * CH];
-                    const f2 dt = pack2(d.x, d.x), u = pack2(d.y, d.y);
-                    const float* q = bc + (t0 + t) * NP * 2;
-                    f2 bv[NH];
-                    if (NS == 1) {
-                        const float2 v = *reinterpret_cast<const float2*>(q);
-                        bv[0] = pack2(v.x, 0.f);
-                        cv[w][t][0] = pack2(v.y, 0.f);
-                    } else if (NS == 2) {
-                        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(q);
-                        bv[0] = v.x;
-                        cv[w][t][0] = v.y;
-                    } else {
+            for (int t = 0; t < NB; ++t) {
+                dv[w][t] = du[(t0 + t) * CH];
+                const float* q = bc + (t0 + t) * NP * 2;
+                if (NS == 1) {
+                    const float2 v = *reinterpret_cast<const float2*>(q);
+                    bv[w][t][0] = pack2(v.x, 0.f);
+                    cv[w][t][0] = pack2(v.y, 0.f);
+                } else if (NS == 2) {
+                    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(q);
+                    bv[w][t][0] = v.x;
+                    cv[w][t][0] = v.y;
+                } else {
 #pragma unroll
-                        for (int i = 0; i < NH; i += 2) {
-                            const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(q + 2 * i);
-                            const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(q + NS + 2 * i);
-                            bv[i] = v.x;
-                            bv[i + (NH > 1)] = v.y;
-                            cv[w][t][i] = x.x;
-                            cv[w][t][i + (NH > 1)] = x.y;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < NH; ++i) {
-                        const float2 e = unpack2(mul2(dt, A2[i]));
-                        dec[w][t][i] = pack2(ex2_approx(e.x), NS > 1 ? ex2_approx(e.y) : 0.f);
-                        add[w][t][i] = mul2(u, bv[i]);
+                    for (int i = 0; i < NH; i += 2) {
+                        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(q + 2 * i);
+                        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(q + NS + 2 * i);
+                        bv[w][t][i] = v.x;
+                        bv[w][t][i + (NH > 1)] = v.y;
+                        cv[w][t][i] = x.x;
+                        cv[w][t][i + (NH > 1)] = x.y;
                     }
                 }
-            };
-            named_bar(kReady + (k & 1), kThreads);
-            take(0, 0);
+            }
+        };
+        auto decays = [&](int t, int w) {
+            const f2 dt = pack2(dv[w][t].x, dv[w][t].x);
+#pragma unroll
+            for (int i = 0; i < NH; ++i) {
+                const float2 e = unpack2(mul2(dt, A2[i]));
+                dec[w][t][i] = pack2(ex2_approx(e.x), NS > 1 ? ex2_approx(e.y) : 0.f);
+            }
+        };
+        for (int k = 0; k < nt; ++k) {
+            float* yp = reinterpret_cast<float*>(sm + P::OFF_BUF + (k % kBufs) * P::BUF + P::DU + P::BCF) + l * P::YP + ch;
+            named_bar(kReady + k % kBufs, kThreads);
+            load(k, 0, 0);
+#pragma unroll
+            for (int t = 0; t < NB; ++t) decays(t, 0);
 #pragma unroll
             for (int t0 = 0; t0 < TT; t0 += NB) {
                 const int w = t0 / NB & 1;
-                if (t0 + NB < TT) take(t0 + NB, w ^ 1);
+                const bool more = t0 + NB < TT;
+                if (more) load(k, t0 + NB, w ^ 1);
 #pragma unroll
                 for (int t = 0; t < NB; ++t) {
+                    const f2 u = pack2(dv[w][t].y, dv[w][t].y);
                     f2 acc = 0;
 #pragma unroll
                     for (int i = 0; i < NH; ++i) {
-                        h[i] = fma2(dec[w][t][i], h[i], add[w][t][i]);
+                        h[i] = fma2(dec[w][t][i], h[i], mul2(u, bv[w][t][i]));
                         acc = i == 0 ? mul2(cv[w][t][i], h[i]) : fma2(cv[w][t][i], h[i], acc);
                     }
+                    if (more) decays(t, w ^ 1);
                     if (!SUMMARY) {
                         const float2 q = unpack2(acc);
                         yp[(t0 + t) * P::YROW] = q.x + q.y;
                     }
                 }
             }
-            bar_arrive(kDone + (k & 1), kThreads);
+            bar_arrive(kDone + k % kBufs, kThreads);
         }
         if (SUMMARY) {
             float* slot = a.workspace + (unit0 + seg) * slot_floats<NS, LANES>();
@@ -411,22 +418,24 @@ ssm_scan_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ Lens 
             }
         };
 #pragma unroll
-        for (int k = 0; k < kRaw - 3; ++k) fetch(k);
+        for (int k = 0; k < kRaw - kBufs - 1; ++k) fetch(k);
         for (int k = 0; k < nt; ++k) {
-            // tile k - 2 is through the recurrence (its buffer is free) and tile k - 3 is finished (its raw rows are free)
-            if (k >= 2) named_bar(kDone + (k & 1), kThreads);
-            cp_async_wait<kRaw - 4>();
+            // tile k - kBufs is through the recurrence (its buffer is free) and the one before it is finished (its raw
+            // rows are free)
+            if (k >= kBufs) named_bar(kDone + k % kBufs, kThreads);
+            cp_async_wait<kRaw - kBufs - 2>();
             named_bar(kPrepBar, kPrep);               // tile k is in shared memory for every preparing thread
             const unsigned char* st = raw(k);
-            unsigned char* buf = sm + P::OFF_BUF + (k & 1) * P::BUF;
+            unsigned char* buf = sm + P::OFF_BUF + (k % kBufs) * P::BUF;
             const T* xs = (const T*)st;
             const T* ds = (const T*)(st + P::ROW);
             float2* du = reinterpret_cast<float2*>(buf);
             const int rows = s1 - s0 - k * TT;
             spread(reinterpret_cast<float*>(buf + P::DU), (const T*)(st + 3 * P::ROW), (const T*)(st + 3 * P::ROW + P::BC));
 #pragma unroll
-            for (int i = 0; i < TT / TR; ++i) {
+            for (int i = 0; i < (TT + TR - 1) / TR; ++i) {
                 const int t = tr + i * TR;
+                if (TR > TT && t >= TT) break;
                 const float2 d2 = load2<T>(ds + t * CH + cc), x2 = load2<T>(xs + t * CH + cc);
                 float dt[2] = {d2.x + bias[0], d2.y + bias[1]};
 #pragma unroll
@@ -437,11 +446,11 @@ ssm_scan_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ Lens 
                 }
                 *reinterpret_cast<float4*>(du + t * CH + cc) = make_float4(dt[0], dt[0] * x2.x, dt[1], dt[1] * x2.y);
             }
-            bar_arrive(kReady + (k & 1), kThreads);
-            fetch(k + kRaw - 3);                          // into the rows of tile k - 3
+            bar_arrive(kReady + k % kBufs, kThreads);
+            fetch(k + kRaw - kBufs - 1);                  // into the rows of tile k - kBufs - 1
         }
         // the barriers that the other threads still pass
-        for (int k = max(nt, 2); k < nt + 2; ++k) named_bar(kDone + (k & 1), kThreads);
+        for (int k = max(nt, kBufs); k < nt + kBufs; ++k) named_bar(kDone + k % kBufs, kThreads);
         if (SUMMARY) {
             // sum of dt over the threads of each channel
             named_bar(kPrepBar, kPrep);
@@ -466,18 +475,19 @@ ssm_scan_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ Lens 
         // rows of out that take two values in one store
         const bool pairs = a.D % 2 == 0 && c0 % 2 == 0 && nch % 2 == 0 && reinterpret_cast<uintptr_t>(a.out) % (2 * sizeof(T)) == 0;
         T* op = (T*)a.out + ((size_t)b * a.N + s0) * a.D + c0 + cc;
-        for (int k = 0; k < min(nt, 2); ++k) bar_arrive(kReady + k, kThreads);     // the y parts are free
+        for (int k = 0; k < min(nt, kBufs); ++k) bar_arrive(kReady + k, kThreads);     // the y parts are free
         for (int k = 0; k < nt; ++k) {
-            named_bar(kDone + (k & 1), kThreads);
+            named_bar(kDone + k % kBufs, kThreads);
             if (!SUMMARY) {
                 const unsigned char* st = sm + (k % kRaw) * P::STAGE;
-                const float* yp = reinterpret_cast<const float*>(sm + P::OFF_BUF + (k & 1) * P::BUF + P::DU + P::BCF) + cc;
+                const float* yp = reinterpret_cast<const float*>(sm + P::OFF_BUF + (k % kBufs) * P::BUF + P::DU + P::BCF) + cc;
                 const T* xs = (const T*)st;
                 const T* zs = (const T*)(st + 2 * P::ROW);
                 const int rows = s1 - s0 - k * TT;
 #pragma unroll 4
-                for (int i = 0; i < TT / TR; ++i) {
+                for (int i = 0; i < (TT + TR - 1) / TR; ++i) {
                     const int t = tr + i * TR;
+                    if (TR > TT && t >= TT) break;
                     const float2 x2 = load2<T>(xs + t * CH + cc);
                     float y[2] = {0.f, 0.f};
 #pragma unroll
@@ -501,7 +511,7 @@ ssm_scan_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ Lens 
                     }
                 }
             }
-            if (k + 2 < nt) bar_arrive(kReady + (k & 1), kThreads);
+            if (k + kBufs < nt) bar_arrive(kReady + k % kBufs, kThreads);
         }
     }
 }
@@ -539,13 +549,13 @@ cudaError_t launch_scan_ns(const SsmArgs& a)
     if (err != cudaSuccess) return err;
     int stage = 0;
     if (a.segs > 1) {
-        sum_k<<<dim3(tpg * a.G, a.segs - 1, a.B), kThreads, P::BYTES, a.stream>>>(a, lens, tpg, px, pb);
+        sum_k<<<dim3(tpg * a.G, a.segs - 1, a.B), P::THREADS, P::BYTES, a.stream>>>(a, lens, tpg, px, pb);
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
         stage_mark(stage++, a.stream);
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(tpg * a.G, a.segs, a.B);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(P::THREADS);
     cfg.dynamicSmemBytes = P::BYTES;
     cfg.stream = a.stream;
     cudaLaunchAttribute attr{};
@@ -557,9 +567,6 @@ cudaError_t launch_scan_ns(const SsmArgs& a)
     if (err == cudaSuccess) stage_mark(stage, a.stream);
     return err;
 }
-
-// Lanes a channel: four, eight where sixteen states a lane would not fit its registers.
-int lanes_for(int n) { return n > 32 ? 8 : 4; }
 
 template <typename T>
 cudaError_t launch_scan_t(const SsmArgs& a)
@@ -575,8 +582,7 @@ cudaError_t launch_scan_t(const SsmArgs& a)
 
 void ssm_scan_segments(int B, int N, int D, int G, int n, int* segs, int* seg_len)
 {
-    const int ch = kRec / lanes_for(n);
-    const long long units = (long long)B * G * ((D / G + ch - 1) / ch);
+    const long long units = (long long)B * G * ((D / G + kCh - 1) / kCh);
     int g = 1;
     // a segment more than one costs a second pass over the exponentials
     if (units < 60) g = (int)max(1ll, min(min(148 / units, (long long)N / 128), 64ll));
@@ -591,8 +597,7 @@ size_t ssm_scan_workspace_bytes(int B, int N, int D, int G, int n)
     ssm_scan_segments(B, N, D, G, n, &segs, &len);
     if (segs <= 1) return 0;
     const int np = n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 64;
-    const int ch = kRec / lanes_for(n);
-    return (size_t)B * G * ((D / G + ch - 1) / ch) * segs * ch * (np + 1) * sizeof(float);
+    return (size_t)B * G * ((D / G + kCh - 1) / kCh) * segs * kCh * (np + 1) * sizeof(float);
 }
 
 cudaError_t launch_ssm_scan(const SsmArgs& a)
