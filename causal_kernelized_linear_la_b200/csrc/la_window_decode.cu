@@ -158,16 +158,252 @@ window_decode_simt(const __grid_constant__ WindowArgs a, int chunks)
     cluster.sync();   // the others' shared memory stays until everyone has read it
 }
 
-template <typename T, int D, int DV>
-cudaError_t launch_simt(const WindowArgs& a)
+// ---------------------------------------------------------------------------
+// bf16 on the tensor cores' warp instructions (mma m16n8k16): eight query
+// heads of a kv head are the N of both products, so grouped heads cost no more
+// than one,
+//     S^T = K Q^T   (16 keys x 8 heads, K-axis d)
+//     O^T += V^T P^T   (dv x 8 heads, K-axis 16 keys)
+// and one register operand per product comes straight from global memory:
+// the order of an MMA's K-axis and of its M rows is free as long as both
+// operands, or the output, follow it.
+//   K: lane (g, t) takes 16 bytes at d = 32 s + 8 t of the keys g and g + 8; its
+//      four 32-bit words are the K-slots (2t, 2t+1), (2t+8, 2t+9) of the steps
+//      2 s and 2 s + 1, and q is loaded with the same map.
+//   V: lane (g, t) takes 16 bytes at column 64 c + 8 g of the keys 2t, 2t+1, 2t+8,
+//      2t+9; byte permutes pair the keys, and row g (g + 8) of output tile
+//      4 c + j is column 64 c + 8 g + 2 j (+ 1).
+// No shared memory is staged: each warp keeps one block of 16 keys of K and V
+// in flight, twelve warps an SM some 90 KB.  The weights are rounded to bf16
+// for the second product (2^-8 at most, as V is held).
+constexpr int kMmaHeads = 8;
+constexpr int kMmaWarps = 4;
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1)
 {
-    const int group = a.Hq / a.Hkv, chunks = (group + kHeads - 1) / kHeads;
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 8 x 8 fragment of 16-bit values -> the fragment of its transpose
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint4 load_stream(const __nv_bfloat16* p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// grid: (splits, Hkv * head chunks, sequences), clusters along x
+template <int D, int DV>
+__global__ void __launch_bounds__(kMmaWarps * 32, 3)
+window_decode_mma(const __grid_constant__ WindowArgs a, int chunks)
+{
+    constexpr int KS = D / 32, VC = DV / 64, OT = DV / 16;   // 16-byte pieces of a K row, of a V row per lane; output tiles
+    constexpr int OP = DV + 4;                               // row pitch of the partial outputs
+    __shared__ float part_o[kMmaWarps][kMmaHeads][OP];
+    __shared__ float part_ml[kMmaWarps + 1][kMmaHeads][2];   // the last: of the whole CTA
+    cg::cluster_group cluster = cg::this_cluster();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int split = blockIdx.x, splits = gridDim.x, b = blockIdx.z;
+    const int kvh = blockIdx.y / chunks, chunk = blockIdx.y % chunks;
+    const int group = a.Hq / a.Hkv;
+    const int h0 = kvh * group + chunk * kMmaHeads, nh = min(kMmaHeads, group - chunk * kMmaHeads);
+    const int pos = a.pos[b];
+    if (pos < 0) return;        // an idle sequence: the whole cluster leaves
+    const int cap = a.window + a.sinks;
+    const int used = pos < cap ? pos + 1 : cap;
+    const int slot_new = pos < a.sinks ? pos : a.sinks + (pos - a.sinks) % a.window;
+    const int per = ((used + splits - 1) / splits + 15) / 16 * 16;
+    const int s0 = min(used, split * per), s1 = min(used, s0 + per);
+
+    const size_t kv = (size_t)b * a.Hkv + kvh;
+    __nv_bfloat16* kc = (__nv_bfloat16*)a.k_cache + kv * cap * D;
+    __nv_bfloat16* vc = (__nv_bfloat16*)a.v_cache + kv * cap * DV;
+    const __nv_bfloat16* kn = (const __nv_bfloat16*)a.k + b * a.st.k_batch + kvh * a.st.k_head;
+    const __nv_bfloat16* vn = (const __nv_bfloat16*)a.v + b * a.st.v_batch + kvh * a.st.v_head;
+    const float sl = a.scale * kLog2e;
+
+    uint4 kr[2][KS], vr[4][VC];
+    // slots past the run repeat its last one, whose values are finite; their weights are zero
+    auto k_row = [&](int s) { const int x = min(s, s1 - 1); return (x == slot_new ? kn : kc + (size_t)x * D) + 8 * t; };
+    auto v_row = [&](int s) { const int x = min(s, s1 - 1); return (x == slot_new ? vn : vc + (size_t)x * DV) + 8 * g; };
+    auto load_k = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const __nv_bfloat16* p = k_row(s + g + 8 * i);
+#pragma unroll
+            for (int x = 0; x < KS; ++x) kr[i][x] = load_stream(p + 32 * x);
+        }
+    };
+    auto load_v = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat16* p = v_row(s + 2 * t + (i & 1) + 8 * (i >> 1));
+#pragma unroll
+            for (int x = 0; x < VC; ++x) vr[i][x] = load_stream(p + 64 * x);
+        }
+    };
+
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // of heads 2t, 2t+1 (l: this lane's keys)
+    float o[OT][4];
+#pragma unroll
+    for (int j = 0; j < OT; ++j)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[j][x] = 0.f;
+    int s = s0 + warp * 16;
+    if (s < s1) {
+        load_k(s);
+        load_v(s);
+    }
+    uint4 qr[KS];
+#pragma unroll
+    for (int x = 0; x < KS; ++x) {
+        qr[x] = make_uint4(0u, 0u, 0u, 0u);
+        if (g < nh)
+            qr[x] = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q + b * a.st.q_batch + (h0 + g) * a.st.q_head + 32 * x + 8 * t);
+    }
+    for (; s < s1; s += kMmaWarps * 16) {
+        const int next = s + kMmaWarps * 16;
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < KS; ++x) {
+            mma_16816(c, kr[0][x].x, kr[1][x].x, kr[0][x].y, kr[1][x].y, qr[x].x, qr[x].y);
+            mma_16816(c, kr[0][x].z, kr[1][x].z, kr[0][x].w, kr[1][x].w, qr[x].z, qr[x].w);
+        }
+        if (next < s1) load_k(next);
+        // c: keys g (0, 1) and g + 8 (2, 3) of heads 2t, 2t + 1
+        const bool on0 = s + g < s1, on1 = s + g + 8 < s1;
+        float top[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            c[j] = on0 ? c[j] * sl : -INFINITY;
+            c[2 + j] = on1 ? c[2 + j] * sl : -INFINITY;
+            top[j] = fmaxf(c[j], c[2 + j]);
+#pragma unroll
+            for (int w = 4; w < 32; w *= 2) top[j] = fmaxf(top[j], __shfl_xor_sync(~0u, top[j], w));
+        }
+        if (__any_sync(~0u, top[0] > m[0] || top[1] > m[1])) {
+            float f[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float nm = fmaxf(m[j], top[j]);
+                f[j] = m[j] == -INFINITY ? 0.f : exp2f(m[j] - nm);
+                m[j] = nm;
+                l[j] *= f[j];
+            }
+#pragma unroll
+            for (int j = 0; j < OT; ++j) {
+                o[j][0] *= f[0];
+                o[j][1] *= f[1];
+                o[j][2] *= f[0];
+                o[j][3] *= f[1];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float ref = m[j] == -INFINITY ? 0.f : m[j];
+            c[j] = exp2f(c[j] - ref);
+            c[2 + j] = exp2f(c[2 + j] - ref);
+            l[j] += c[j] + c[2 + j];
+        }
+        const uint32_t p0 = transpose8(bf16_pair(c[0], c[1])), p1 = transpose8(bf16_pair(c[2], c[3]));
+#pragma unroll
+        for (int x = 0; x < VC; ++x) {
+            const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vr[0][x]);
+            const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vr[1][x]);
+            const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vr[2][x]);
+            const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vr[3][x]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                mma_16816(o[4 * x + j], __byte_perm(v0[j], v1[j], 0x5410), __byte_perm(v0[j], v1[j], 0x7632),
+                          __byte_perm(v2[j], v3[j], 0x5410), __byte_perm(v2[j], v3[j], 0x7632), p0, p1);
+        }
+        if (next < s1) load_v(next);
+    }
+    // the new token takes its slot; every reader of the slot reads kn, vn
+    if (s0 <= slot_new && slot_new < s1 && chunk == 0) {
+        if (tid < D / 8) reinterpret_cast<uint4*>(kc + (size_t)slot_new * D)[tid] = reinterpret_cast<const uint4*>(kn)[tid];
+        if (tid < DV / 8) reinterpret_cast<uint4*>(vc + (size_t)slot_new * DV)[tid] = reinterpret_cast<const uint4*>(vn)[tid];
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int w = 4; w < 32; w *= 2) l[j] += __shfl_xor_sync(~0u, l[j], w);
+        if (g == 0) {
+            part_ml[warp][2 * t + j][0] = m[j];
+            part_ml[warp][2 * t + j][1] = l[j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < OT; ++j) {
+        const int col = 64 * (j / 4) + 8 * g + 2 * (j % 4);
+        *reinterpret_cast<float2*>(&part_o[warp][2 * t][col]) = make_float2(o[j][0], o[j][2]);
+        *reinterpret_cast<float2*>(&part_o[warp][2 * t + 1][col]) = make_float2(o[j][1], o[j][3]);
+    }
+    __syncthreads();
+    // the warps' parts into warp 0's place
+    for (int e = tid; e < nh * DV; e += kMmaWarps * 32) {
+        const int h = e / DV, c = e % DV;
+        float top = -INFINITY, sum = 0.f, acc = 0.f;
+#pragma unroll
+        for (int w = 0; w < kMmaWarps; ++w) top = fmaxf(top, part_ml[w][h][0]);
+        const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int w = 0; w < kMmaWarps; ++w) {
+            const float f = exp2f(part_ml[w][h][0] - ref);
+            sum = fmaf(part_ml[w][h][1], f, sum);
+            acc = fmaf(part_o[w][h][c], f, acc);
+        }
+        if (splits == 1) {
+            ((__nv_bfloat16*)a.out)[b * a.st.out_batch + (h0 + h) * a.st.out_head + c] = __float2bfloat16_rn(acc / sum);
+        } else {
+            part_o[0][h][c] = acc;       // this thread alone reads and writes column c of head h
+            if (c == 0) {
+                part_ml[kMmaWarps][h][0] = top;
+                part_ml[kMmaWarps][h][1] = sum;
+            }
+        }
+    }
+    if (splits == 1) return;
+    cluster.sync();
+    for (int e = split * kMmaWarps * 32 + tid; e < nh * DV; e += splits * kMmaWarps * 32) {
+        const int h = e / DV, c = e % DV;
+        float top = -INFINITY, sum = 0.f, acc = 0.f;
+        for (int r = 0; r < splits; ++r) top = fmaxf(top, cluster.map_shared_rank(&part_ml[kMmaWarps][h][0], r)[0]);
+        for (int r = 0; r < splits; ++r) {
+            const float f = exp2f(cluster.map_shared_rank(&part_ml[kMmaWarps][h][0], r)[0] - top);
+            sum = fmaf(cluster.map_shared_rank(&part_ml[kMmaWarps][h][1], r)[0], f, sum);
+            acc = fmaf(cluster.map_shared_rank(&part_o[0][h][c], r)[0], f, acc);
+        }
+        ((__nv_bfloat16*)a.out)[b * a.st.out_batch + (h0 + h) * a.st.out_head + c] = __float2bfloat16_rn(acc / sum);
+    }
+    cluster.sync();   // the others' shared memory stays until everyone has read it
+}
+
+// One launch: clusters of `splits` CTAs share a (sequence, kv head, head chunk).
+template <typename F>
+cudaError_t launch_clusters(F kern, const WindowArgs& a, int heads, int threads, int least)
+{
+    const int group = a.Hq / a.Hkv, chunks = (group + heads - 1) / heads;
     const long long units = (long long)a.B * a.Hkv * chunks;
     int splits = 1;
-    while (splits < kMaxSplit && units * splits < 296 && (a.window + a.sinks) / (splits * 2) >= 64) splits *= 2;
+    while (splits < kMaxSplit && units * splits < 148 * 4 && (a.window + a.sinks) / (splits * 2) >= least) splits *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(splits, a.Hkv * chunks, a.B);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.stream = a.stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -175,21 +411,22 @@ cudaError_t launch_simt(const WindowArgs& a)
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, window_decode_simt<T, D, DV>, a, chunks);
+    return cudaLaunchKernelEx(&cfg, kern, a, chunks);
 }
 
-template <typename T>
-cudaError_t launch_t(const WindowArgs& a)
+template <int D, int DV>
+cudaError_t launch_dd(const WindowArgs& a)
 {
-    if (a.d == 64) return a.dv == 64 ? launch_simt<T, 64, 64>(a) : launch_simt<T, 64, 128>(a);
-    return a.dv == 64 ? launch_simt<T, 128, 64>(a) : launch_simt<T, 128, 128>(a);
+    if (a.dtype == LA_BF16) return launch_clusters(window_decode_mma<D, DV>, a, kMmaHeads, kMmaWarps * 32, 64);
+    return launch_clusters(window_decode_simt<float, D, DV>, a, kHeads, kThreads, 64);
 }
 
 }  // namespace
 
 cudaError_t launch_window_decode(const WindowArgs& a)
 {
-    return a.dtype == LA_BF16 ? launch_t<__nv_bfloat16>(a) : launch_t<float>(a);
+    if (a.d == 64) return a.dv == 64 ? launch_dd<64, 64>(a) : launch_dd<64, 128>(a);
+    return a.dv == 64 ? launch_dd<128, 64>(a) : launch_dd<128, 128>(a);
 }
 
 }  // namespace la
