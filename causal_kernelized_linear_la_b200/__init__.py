@@ -341,17 +341,22 @@ def la_causal_conv(x, weight, cache=None, out=None, cache_out=None, stream=None)
 def _on_device(first, others, stream):
     """Checks that every tensor is on the first one's CUDA device; returns that
     device's (given or current) stream handle and the device guard of the call."""
-    torch = _torch()
-    dev = first.device
-    if dev.type != "cuda":
+    cuda = _torch().cuda
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("all tensors must be CUDA tensors (the library has no CPU path)")
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on one CUDA device, got {dev} and {t.device}")
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    if s.device != dev:
-        raise ValueError(f"the stream is on {s.device}, the tensors on {dev}")
-    return s.cuda_stream, torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else _NO_GUARD
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"all tensors must be on one CUDA device, got {first.device} and {t.device}")
+    if stream is None:
+        # the handle alone where torch offers it: half the cost of a Stream object
+        raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+        handle = raw(dev) if raw is not None else cuda.current_stream(dev).cuda_stream
+    elif stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
+    else:
+        handle = stream.cuda_stream
+    return handle, _NO_GUARD if dev == cuda.current_device() else cuda.device(dev)
 
 
 _NO_GUARD = contextlib.nullcontext()
@@ -379,24 +384,32 @@ def _addr(t):
 
 
 def _group_of(t, lead, D, name):
-    """(tensor as [..., G, n], G, n) of B or C given as [..., n] or [..., G, n]."""
-    if t.dim() == len(lead) + 1:
-        t = t.unsqueeze(-2)
-    if t.dim() != len(lead) + 2 or t.shape[:-2] != lead:
-        raise ValueError(f"{name} must be [{', '.join(map(str, lead))}, G, n] (or without G), got {list(t.shape)}")
-    G, n = t.shape[-2:]
-    if (n > 1 and t.stride(-1) != 1) or (G > 1 and t.stride(-2) != n):
+    """(G, n, batch stride, row stride) of B or C given as [*lead, n] or [*lead, G, n]."""
+    shape, stride, k = t.shape, t.stride(), len(lead)
+    if len(shape) == k + 1:
+        G, n = 1, shape[k]
+    elif len(shape) == k + 2:
+        G, n = shape[k], shape[k + 1]
+        if G > 1 and stride[k] != n:
+            raise ValueError(f"the G * n values of a row of {name} must be contiguous")
+    else:
+        G = n = 0
+    if n == 0 or shape[:k] != lead:
+        raise ValueError(f"{name} must be [{', '.join(map(str, lead))}, G, n] (or without G), got {list(shape)}")
+    if n > 1 and stride[-1] != 1:
         raise ValueError(f"the G * n values of a row of {name} must be contiguous")
     if G == 0 or D % G:
         raise ValueError(f"{name} has {G} groups for {D} channels")
-    return t, G, n
+    # an axis of one entry has no stride that matters
+    return G, n, stride[0] if shape[0] > 1 else 0, stride[1] if k > 1 and shape[1] > 1 else 0
 
 
 def _row_stride(t, name):
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    """(batch stride, row stride) of [B, D] or [B, N, D]."""
+    shape, stride = t.shape, t.stride()
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"the last axis of {name} must be contiguous")
-    # an axis of one entry has no stride that matters
-    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.dim() > 2 and t.shape[1] > 1 else 0
+    return stride[0] if shape[0] > 1 else 0, stride[1] if len(shape) > 2 and shape[1] > 1 else 0
 
 
 def _lens_of(seq_lens, B):
@@ -445,26 +458,28 @@ def la_ssm_scan_workspace_bytes(B, N, D, G, n) -> int:
     return int(lib().la_ssm_scan_workspace_bytes(B, N, D, G, n))
 
 
-def _ssm_checks(x, delta, A, B, C, D, z, delta_bias, rows):
+def _ssm_checks(x, delta, A, B, C, D, z, delta_bias):
     """Shapes and strides shared by the prompt scan and the token step."""
     torch = _torch()
-    ch = x.shape[-1]
-    if delta.shape != x.shape or (z is not None and z.shape != x.shape):
-        raise ValueError(f"delta and z must have the shape of x, {list(x.shape)}")
-    Bt, G, n = _group_of(B, x.shape[:-1], ch, "B")
-    Ct, G2, n2 = _group_of(C, x.shape[:-1], ch, "C")
-    if (G, n) != (G2, n2):
+    shape, dtype = x.shape, x.dtype
+    ch = shape[-1]
+    if delta.shape != shape or (z is not None and z.shape != shape):
+        raise ValueError(f"delta and z must have the shape of x, {list(shape)}")
+    G, n, Bb, Br = _group_of(B, shape[:-1], ch, "B")
+    G2, n2, Cb, Cr = _group_of(C, shape[:-1], ch, "C")
+    if G != G2 or n != n2:
         raise ValueError(f"B and C differ: {G} x {n} and {G2} x {n2}")
-    for t, name in ((delta, "delta"), (B, "B"), (C, "C"), (z, "z")):
-        if t is not None and t.dtype != x.dtype:
-            raise ValueError(f"x, delta, B, C and z must have one dtype; {name} has {t.dtype}")
+    if not (delta.dtype == dtype and B.dtype == dtype and C.dtype == dtype and (z is None or z.dtype == dtype)):
+        raise ValueError("x, delta, B, C and z must have one dtype")
     _dense(A, (ch, n), torch.float32, "A")
-    for t, name in ((D, "D"), (delta_bias, "delta_bias")):
-        if t is not None:
-            _dense(t, (ch,), torch.float32, name)
-    zs = _row_stride(z, "z") if z is not None else (0, 0)
-    bs, cs = ((t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if rows and t.shape[1] > 1 else 0) for t in (Bt, Ct))
-    return G, n, LaSsmStrides(*_row_stride(x, "x"), *_row_stride(delta, "delta"), *zs, *bs, *cs)
+    if D is not None:
+        _dense(D, (ch,), torch.float32, "D")
+    if delta_bias is not None:
+        _dense(delta_bias, (ch,), torch.float32, "delta_bias")
+    xb, xr = _row_stride(x, "x")
+    db, dr = _row_stride(delta, "delta")
+    zb, zr = _row_stride(z, "z") if z is not None else (0, 0)
+    return G, n, LaSsmStrides(xb, xr, db, dr, zb, zr, Bb, Br, Cb, Cr)
 
 
 def la_ssm_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, delta_softplus=False, h0=None, seq_lens=None,
@@ -477,7 +492,7 @@ def la_ssm_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, delta_softpl
     if x.dim() != 3:
         raise ValueError("x must be [B,N,D]")
     b, N, ch = x.shape
-    G, n, st = _ssm_checks(x, delta, A, B, C, D, z, delta_bias, True)
+    G, n, st = _ssm_checks(x, delta, A, B, C, D, z, delta_bias)
     if out is None:
         out = _new((b, N, ch), x.dtype, x.device, stream)
     if h_out is None:
@@ -511,7 +526,7 @@ def la_ssm_step(x, delta, A, B, C, h, D=None, z=None, delta_bias=None, delta_sof
     if x.dim() != 2:
         raise ValueError("x must be [B,D]")
     b, ch = x.shape
-    G, n, st = _ssm_checks(x, delta, A, B, C, D, z, delta_bias, False)
+    G, n, st = _ssm_checks(x, delta, A, B, C, D, z, delta_bias)
     if out is None:
         out = _new((b, ch), x.dtype, x.device, stream)
     _dense(out, (b, ch), x.dtype, "out")
@@ -527,30 +542,36 @@ def la_ssm_step(x, delta, A, B, C, h, D=None, z=None, delta_bias=None, delta_sof
     return out
 
 
+def _head_strides(t, rows, name):
+    """(batch, head, row) strides of [B, H, N, .] (rows) or [B, H, .]; an axis of one entry has none that matters."""
+    shape, stride = t.shape, t.stride()
+    if stride[-1] != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    return (stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0,
+            stride[2] if rows and shape[2] > 1 else 0)
+
+
 def _window_checks(q, k, v, out, k_cache, v_cache, pos, window, sinks, scale):
-    """Shapes of both window calls (trailing axes; decode has no token axis)."""
-    torch = _torch()
-    B, Hq, d = q.shape[0], q.shape[1], q.shape[-1]
-    Hkv, dv = k.shape[1], v.shape[-1]
-    if k.shape != (B, Hkv, *q.shape[2:]) or v.shape != (B, Hkv, *q.shape[2:-1], dv):
-        raise ValueError(f"q, k, v do not fit: {list(q.shape)}, {list(k.shape)}, {list(v.shape)}")
-    if out.shape != (*q.shape[:-1], dv):
-        raise ValueError(f"out must be {[*q.shape[:-1], dv]}, got {list(out.shape)}")
-    if not q.dtype == k.dtype == v.dtype == out.dtype:
+    """Shapes of both window calls (decode has no token axis)."""
+    qs, ks, vs, dtype = q.shape, k.shape, v.shape, q.dtype
+    rows = len(qs) == 4
+    B, Hq, d, Hkv, dv = qs[0], qs[1], qs[-1], ks[1], vs[-1]
+    N = qs[2] if rows else 1
+    if ks[0] != B or vs[0] != B or vs[1] != Hkv or ks[-1] != d or (rows and not ks[2] == vs[2] == N):
+        raise ValueError(f"q, k, v do not fit: {list(qs)}, {list(ks)}, {list(vs)}")
+    if out.shape != ((B, Hq, N, dv) if rows else (B, Hq, dv)):
+        raise ValueError(f"out must be {[*qs[:-1], dv]}, got {list(out.shape)}")
+    if not (k.dtype == dtype and v.dtype == dtype and out.dtype == dtype):
         raise ValueError("q, k, v and out must have one dtype")
-    st = []
-    for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out")):
-        if t.stride(-1) != 1:
-            raise ValueError(f"the last axis of {name} must be contiguous")
-        # an axis of one entry has no stride that matters
-        st += [s if n > 1 else 0 for s, n in zip(t.stride()[:-1], t.shape[:-1])] + [0] * (4 - t.dim())
     if k_cache is not None:
-        _dense(k_cache, (B, Hkv, sinks + window, d), q.dtype, "k_cache")
+        _dense(k_cache, (B, Hkv, sinks + window, d), dtype, "k_cache")
     if v_cache is not None:
-        _dense(v_cache, (B, Hkv, sinks + window, dv), q.dtype, "v_cache")
+        _dense(v_cache, (B, Hkv, sinks + window, dv), dtype, "v_cache")
     if pos is not None:
-        _dense(pos, (B,), torch.int32, "pos")
-    return B, Hq, Hkv, d, dv, float(d ** -0.5 if scale is None else scale), LaWindowStrides(*st)
+        _dense(pos, (B,), _torch().int32, "pos")
+    st = LaWindowStrides(*_head_strides(q, rows, "q"), *_head_strides(k, rows, "k"), *_head_strides(v, rows, "v"),
+                         *_head_strides(out, rows, "out"))
+    return B, Hq, Hkv, N, d, dv, float(d ** -0.5 if scale is None else scale), st
 
 
 def la_window_prefill(q, k, v, window, sinks=0, k_cache=None, v_cache=None, pos=None, seq_lens=None, scale=None,
@@ -565,12 +586,12 @@ def la_window_prefill(q, k, v, window, sinks=0, k_cache=None, v_cache=None, pos=
         raise ValueError("q must be [B,Hq,N,d], k [B,Hkv,N,d] and v [B,Hkv,N,dv]")
     if out is None:
         out = _new((*q.shape[:-1], v.shape[-1]), q.dtype, q.device, stream)
-    B, Hq, Hkv, d, dv, scale, st = _window_checks(q, k, v, out, k_cache, v_cache, pos, window, sinks, scale)
+    B, Hq, Hkv, N, d, dv, scale, st = _window_checks(q, k, v, out, k_cache, v_cache, pos, window, sinks, scale)
     cfg = LaConfig(_dtype_code(q), 0, 0.0, None, None, None, None, 0)
     cfg.stream, guard = _on_device(q, (k, v, out, k_cache, v_cache, pos), stream)
     with guard:
         rc = lib().la_window_prefill(_addr(q), _addr(k), _addr(v), _addr(out), _addr(k_cache), _addr(v_cache),
-                                     _addr(pos), _lens_of(seq_lens, B), B, Hq, Hkv, q.shape[2], d, dv, window, sinks,
+                                     _addr(pos), _lens_of(seq_lens, B), B, Hq, Hkv, N, d, dv, window, sinks,
                                      scale, ctypes.byref(st), ctypes.byref(cfg))
     if rc != LA_OK:
         raise LaError(rc, "la_window_prefill")
@@ -585,7 +606,7 @@ def la_window_decode_step(q, k, v, k_cache, v_cache, pos, window, sinks=0, scale
         raise ValueError("q must be [B,Hq,d], k [B,Hkv,d] and v [B,Hkv,dv]")
     if out is None:
         out = _new((*q.shape[:-1], v.shape[-1]), q.dtype, q.device, stream)
-    B, Hq, Hkv, d, dv, scale, st = _window_checks(q, k, v, out, k_cache, v_cache, pos, window, sinks, scale)
+    B, Hq, Hkv, N, d, dv, scale, st = _window_checks(q, k, v, out, k_cache, v_cache, pos, window, sinks, scale)
     cfg = LaConfig(_dtype_code(q), 0, 0.0, None, None, None, None, 0)
     cfg.stream, guard = _on_device(q, (k, v, out, k_cache, v_cache, pos), stream)
     with guard:

@@ -8,20 +8,25 @@
 // silu(y) = y / (1 + e^-y).
 //
 // Memory-bound: one read of x and one write of y.  A thread owns V channels
-// (8 as 16-byte accesses, or 1 where a row does not start on 16 bytes or D is
-// no multiple of 8) of a run of consecutive tokens, which it takes in batches
-// of kBatch rows: the window of the last w-1 rows stays in registers from
-// batch to batch, and a batch's rows are requested before the previous batch
-// is computed.  Threads are numbered channel groups first, so a warp reads 512
-// consecutive bytes of a row.  Arithmetic is fp32 FMA in tap order from the
-// bias up, rounded to the storage type once.
+// (8 or 4 as accesses of 16 or 8 bytes, 1 where rows do not start on that or D
+// is no multiple of it).  Threads are numbered channel groups first, so a warp
+// reads 512 consecutive bytes of a row.  Arithmetic is fp32 FMA in tap order
+// from the bias up, rounded to the storage type once.
+//
+// Prompts: a thread walks a run of tokens and keeps w-1 unfinished outputs
+// instead of a window of inputs: each row is converted once and added to the w
+// outputs it belongs to, in the order of their taps.  Two half-batches of rows
+// alternate, so that four to eight 16-byte loads of a thread are always in
+// flight.  One token a sequence: a thread takes several sequences, so that the
+// filter, larger than a token's rows, is loaded once for them.
 #include "la_internal.cuh"
 
 namespace la {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 8;   // tokens whose rows are in flight at once; at least w-1, so only run 0 reads the cache
+constexpr int kHalf = 4;    // rows of a half-batch
+constexpr int kSeqs = 4;    // sequences a thread takes where each has one token
 
 struct Lens {
     int use;
@@ -30,7 +35,8 @@ struct Lens {
 
 template <typename T, int V> struct Row;
 template <> struct Row<__nv_bfloat16, 8> { uint4 a; };
-template <> struct Row<float, 8> { float4 a, b; };
+template <> struct Row<__nv_bfloat16, 4> { uint2 a; };
+template <> struct Row<float, 4> { float4 a; };
 template <> struct Row<__nv_bfloat16, 1> { __nv_bfloat16 a; };
 template <> struct Row<float, 1> { float a; };
 
@@ -65,97 +71,176 @@ template <typename T> __device__ __forceinline__ float silu(float y);
 template <> __device__ __forceinline__ float silu<float>(float y) { return y / (1.f + expf(-y)); }
 template <> __device__ __forceinline__ float silu<__nv_bfloat16>(float y) { return __fdividef(y, 1.f + __expf(-y)); }
 
-// One thread: V channels of `batches` * kBatch consecutive tokens of one sequence.
+// V channels' filters [V][W] and biases
+template <int W, int V>
+__device__ __forceinline__ void load_filter(const float* __restrict__ weight, const float* __restrict__ bias, int c0,
+                                            float (&wt)[W][V], float (&b0)[V])
+{
+#pragma unroll
+    for (int j = 0; j < V; ++j) b0[j] = bias ? bias[c0 + j] : 0.f;
+    if (V > 1) {
+        float4 raw[V > 1 ? V * W / 4 : 1];
+        const float4* wp = reinterpret_cast<const float4*>(weight + (size_t)c0 * W);
+#pragma unroll
+        for (int i = 0; i < V * W / 4; ++i) raw[i] = wp[i];
+        const float* wf = reinterpret_cast<const float*>(raw);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+            for (int i = 0; i < W; ++i) wt[i][j] = wf[j * W + i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) wt[i][0] = weight[(size_t)c0 * W + i];
+    }
+}
+
+// One thread: V channels of `run` consecutive tokens of one sequence (run a
+// multiple of 2 kHalf, so that runs but the first start past the cache's reach).
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 ssm_conv_kernel(const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
                 const T* cache, T* __restrict__ y, T* cache_out, const __grid_constant__ Lens lens, int N, int D,
-                int groups, int runs, int batches, long long total, long long xb, long long xt, int act)
+                int groups, int runs, int run, long long total, long long xb, long long xt, int act)
 {
     constexpr int HIST = W - 1;
+    static_assert(2 * kHalf >= HIST, "only the first run reads the cache");
     const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
     if (id >= total) return;
     const int cg = (int)(id % groups);
     const long long r = id / groups;
-    const int run = (int)(r % runs), b = (int)(r / runs);
+    const int b = (int)(r / runs);
     const int len = lens.use ? lens.n[b] : N;
     const int c0 = cg * V;
-    const int t0 = run * batches * kBatch, t1 = min(len, t0 + batches * kBatch);
+    const int t0 = (int)(r % runs) * run, t1 = min(len, t0 + run);
     const T* xc = x + b * xb + c0;
     const T* cc = cache ? cache + (size_t)b * HIST * D + c0 : nullptr;
-    T* yc = y + (size_t)b * N * D + c0;
 
     // row k of [cache; x]; rows past the sequence are not read
     auto fetch = [&](int k) {
         if (k >= HIST) return k - HIST < len ? row_load<T, V>(xc + (k - HIST) * xt) : row_zero<T, V>();
         return cc ? row_load<T, V>(cc + (size_t)k * D) : row_zero<T, V>();
     };
-
     Row<T, V> tail[HIST > 0 ? HIST : 1];
-    const bool keeper = cache_out && run == 0;
-    if (HIST > 0 && keeper) {
+    const bool keeper = HIST > 0 && cache_out && t0 == 0;
+    if (t0 < t1) {
+        Row<T, V> rows[2][kHalf], past[HIST > 0 ? HIST : 1];
+#pragma unroll
+        for (int i = 0; i < HIST; ++i) past[i] = fetch(t0 + i);
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int u = 0; u < kHalf; ++u) rows[a][u] = fetch(t0 + HIST + a * kHalf + u);
+        float wt[W][V], b0[V];
+        load_filter<W, V>(weight, bias, c0, wt, b0);
+        // acc[k]: the output k tokens ahead of the next row
+        float acc[W][V];
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[k][j] = b0[j];
+        auto add = [&](const Row<T, V>& row) {
+            float f[V];
+            row_f32<T, V>(row, f);
+#pragma unroll
+            for (int k = 0; k < W; ++k)
+#pragma unroll
+                for (int j = 0; j < V; ++j) acc[k][j] = fmaf(wt[W - 1 - k][j], f[j], acc[k][j]);
+        };
+        auto shift = [&]() {
+#pragma unroll
+            for (int k = 0; k + 1 < W; ++k)
+#pragma unroll
+                for (int j = 0; j < V; ++j) acc[k][j] = acc[k + 1][j];
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[W - 1][j] = b0[j];
+        };
+        // the history: row t0 + i is tap i of the first output (acc[0] after HIST shifts)
+#pragma unroll
+        for (int i = 0; i < HIST; ++i) {
+            add(past[i]);
+            shift();
+        }
+        T* yp = y + ((size_t)b * N + t0) * D + c0;
+        for (int t = t0; t < t1; t += 2 * kHalf) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+#pragma unroll
+                for (int u = 0; u < kHalf; ++u) {
+                    add(rows[a][u]);
+                    float out[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) out[j] = act ? silu<T>(acc[0][j]) : acc[0][j];
+                    if (t + a * kHalf + u < t1) row_store<T, V>(yp, out);
+                    yp += D;
+                    shift();
+                }
+                if (t + 2 * kHalf < t1) {
+#pragma unroll
+                    for (int u = 0; u < kHalf; ++u) rows[a][u] = fetch(t + 2 * kHalf + HIST + a * kHalf + u);
+                }
+            }
+        }
+    }
+    // every cache row this sequence's channels need is read by this thread alone,
+    // before it writes: cache_out may be the cache itself
+    if (keeper) {
 #pragma unroll
         for (int i = 0; i < HIST; ++i) tail[i] = fetch(len + i);
-    }
-    if (t0 < t1) {
-        float wt[W][V], b0[V], win[W][V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) b0[j] = bias ? bias[c0 + j] : 0.f;
-        if (V == 8) {
-            float4 raw[2 * W];
-            const float4* wp = reinterpret_cast<const float4*>(weight + (size_t)c0 * W);
-#pragma unroll
-            for (int i = 0; i < 2 * W; ++i) raw[i] = wp[i];
-            const float* wf = reinterpret_cast<const float*>(raw);
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-#pragma unroll
-                for (int i = 0; i < W; ++i) wt[i][j] = wf[j * W + i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < W; ++i) wt[i][0] = weight[(size_t)c0 * W + i];
-        }
-        Row<T, V> next[kBatch];
-#pragma unroll
-        for (int i = 0; i < HIST; ++i) row_f32<T, V>(fetch(t0 + i), win[i]);
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) next[u] = fetch(t0 + HIST + u);
-        for (int t = t0; t < t1; t += kBatch) {
-            Row<T, V> rows[kBatch];
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) rows[u] = next[u];
-            if (t + kBatch < t1) {
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) next[u] = fetch(t + kBatch + HIST + u);
-            }
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                row_f32<T, V>(rows[u], win[HIST]);
-                float acc[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) acc[j] = b0[j];
-#pragma unroll
-                for (int i = 0; i < W; ++i)
-#pragma unroll
-                    for (int j = 0; j < V; ++j) acc[j] = fmaf(wt[i][j], win[i][j], acc[j]);
-                if (act) {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) acc[j] = silu<T>(acc[j]);
-                }
-                if (t + u < t1) row_store<T, V>(yc + (size_t)(t + u) * D, acc);
-#pragma unroll
-                for (int i = 0; i < HIST; ++i)
-#pragma unroll
-                    for (int j = 0; j < V; ++j) win[i][j] = win[i + 1][j];
-            }
-        }
-    }
-    // every cache row this sequence's channels need has been read by this thread:
-    // cache_out may be the cache itself
-    if (HIST > 0 && keeper) {
 #pragma unroll
         for (int i = 0; i < HIST; ++i)
             *reinterpret_cast<Row<T, V>*>(cache_out + ((size_t)b * HIST + i) * D + c0) = tail[i];
+    }
+}
+
+// N = 1.  One thread: V channels of kSeqs sequences.
+template <typename T, int W, int V>
+__global__ void __launch_bounds__(kThreads, 3)
+ssm_conv_token_kernel(const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
+                      const T* cache, T* __restrict__ y, T* cache_out, const __grid_constant__ Lens lens, int B, int D,
+                      int groups, int seqs, long long total, long long xb, int act)
+{
+    constexpr int HIST = W - 1;
+    const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
+    if (id >= total) return;
+    const int c0 = (int)(id % groups) * V;
+    const int b0 = (int)(id / groups) * seqs, nb = min(seqs, B - b0);
+    Row<T, V> row[kSeqs][W];
+#pragma unroll
+    for (int s = 0; s < kSeqs; ++s) {
+#pragma unroll
+        for (int i = 0; i < HIST; ++i)
+            row[s][i] = s < nb && cache ? row_load<T, V>(cache + ((size_t)(b0 + s) * HIST + i) * D + c0) : row_zero<T, V>();
+        const bool on = s < nb && !(lens.use && lens.n[b0 + s] == 0);
+        row[s][HIST] = on ? row_load<T, V>(x + (b0 + s) * xb + c0) : row_zero<T, V>();
+    }
+    float wt[W][V], bs[V];
+    load_filter<W, V>(weight, bias, c0, wt, bs);
+#pragma unroll
+    for (int s = 0; s < kSeqs; ++s) {
+        if (s >= nb) break;
+        const bool on = !(lens.use && lens.n[b0 + s] == 0);
+        if (on) {
+            float acc[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[j] = bs[j];
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                float f[V];
+                row_f32<T, V>(row[s][i], f);
+#pragma unroll
+                for (int j = 0; j < V; ++j) acc[j] = fmaf(wt[i][j], f[j], acc[j]);
+            }
+            if (act) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) acc[j] = silu<T>(acc[j]);
+            }
+            row_store<T, V>(y + (size_t)(b0 + s) * D + c0, acc);
+        }
+        if (cache_out) {
+#pragma unroll
+            for (int i = 0; i < HIST; ++i)
+                *reinterpret_cast<Row<T, V>*>(cache_out + ((size_t)(b0 + s) * HIST + i) * D + c0) = on ? row[s][i + 1] : row[s][i];
+        }
     }
 }
 
@@ -167,30 +252,41 @@ cudaError_t launch_v(const SsmConvArgs& a)
     lens.use = a.seq_lens != nullptr;
     if (a.seq_lens)
         for (int b = 0; b < a.B; ++b) lens.n[b] = a.seq_lens[b];
-    // tokens a thread takes: longer runs re-read fewer rows of the window, but
-    // about 148 * 2048 threads have to be left to fill the GPU
-    int batches = 4;
-    while (batches > 1 && (long long)a.B * groups * ((a.N + batches * kBatch - 1) / (batches * kBatch)) < 148ll * 2048)
-        batches /= 2;
-    const int run = batches * kBatch;
+    if (a.N == 1) {
+        // several sequences a thread once there are threads for every SM without that
+        const int seqs = (long long)a.B * groups >= 148ll * 512 ? kSeqs : 1;
+        const long long total = (long long)((a.B + seqs - 1) / seqs) * groups;
+        const long long grid = (total + kThreads - 1) / kThreads;
+        if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+        ssm_conv_token_kernel<T, W, V><<<(unsigned)grid, kThreads, 0, a.stream>>>(
+            (const T*)a.x, a.weight, a.bias, (const T*)a.cache, (T*)a.out, (T*)a.cache_out, lens, a.B, a.D, groups, seqs,
+            total, a.x_batch, a.silu);
+        return cudaGetLastError();
+    }
+    // tokens a thread takes: longer runs re-read fewer rows of the history, but
+    // threads for two waves of every SM have to be left
+    int run = 64;
+    while (run > 2 * kHalf && (long long)a.B * groups * ((a.N + run - 1) / run) < 2 * 148ll * 512) run /= 2;
     const int runs = a.N > 0 ? (a.N + run - 1) / run : 1;
     const long long total = (long long)a.B * groups * runs;
     const long long grid = (total + kThreads - 1) / kThreads;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     ssm_conv_kernel<T, W, V><<<(unsigned)grid, kThreads, 0, a.stream>>>(
-        (const T*)a.x, a.weight, a.bias, (const T*)a.cache, (T*)a.out, (T*)a.cache_out, lens, a.N, a.D, groups, runs,
-        batches, total, a.x_batch, a.x_row, a.silu);
+        (const T*)a.x, a.weight, a.bias, (const T*)a.cache, (T*)a.out, (T*)a.cache_out, lens, a.N, a.D, groups, runs, run,
+        total, a.x_batch, a.x_row, a.silu);
     return cudaGetLastError();
 }
 
 template <typename T, int W>
 cudaError_t launch_w(const SsmConvArgs& a)
 {
-    auto on16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
-    const long long e = sizeof(T);
-    const bool wide = a.D % 8 == 0 && on16(a.x) && on16(a.weight) && on16(a.cache) && on16(a.out) &&
-                      on16(a.cache_out) && a.x_batch * e % 16 == 0 && a.x_row * e % 16 == 0;
-    return wide ? launch_v<T, W, 8>(a) : launch_v<T, W, 1>(a);
+    // channels of a wide thread: 16 bytes of a row, 8 where a longer filter of 8 channels would not fit the registers
+    constexpr int V = 4;
+    constexpr int BYTES = V * (int)sizeof(T);
+    auto on = [](const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+    const bool wide = a.D % V == 0 && on(a.x, BYTES) && on(a.weight, 16) && on(a.cache, BYTES) && on(a.out, BYTES) &&
+                      on(a.cache_out, BYTES) && a.x_batch % V == 0 && a.x_row % V == 0;
+    return wide ? launch_v<T, W, V>(a) : launch_v<T, W, 1>(a);
 }
 
 template <typename T>

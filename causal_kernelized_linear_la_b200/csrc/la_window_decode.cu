@@ -177,7 +177,7 @@ window_decode_simt(const __grid_constant__ WindowArgs a, int chunks)
 // in flight, twelve warps an SM some 90 KB.  The weights are rounded to bf16
 // for the second product (2^-8 at most, as V is held).
 constexpr int kMmaHeads = 8;
-constexpr int kMmaWarps = 4;
+constexpr int kAhead = 2;      // blocks of a warp between an L2 prefetch and its use
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1)
@@ -207,8 +207,8 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b)
 }
 
 // grid: (splits, Hkv * head chunks, sequences), clusters along x
-template <int D, int DV>
-__global__ void __launch_bounds__(kMmaWarps * 32, 3)
+template <int D, int DV, int kMmaWarps>
+__global__ void __launch_bounds__(kMmaWarps * 32, 12 / kMmaWarps)
 window_decode_mma(const __grid_constant__ WindowArgs a, int chunks)
 {
     constexpr int KS = D / 32, VC = DV / 64, OT = DV / 16;   // 16-byte pieces of a K row, of a V row per lane; output tiles
@@ -257,6 +257,13 @@ window_decode_mma(const __grid_constant__ WindowArgs a, int chunks)
         }
     };
 
+    // a block of this warp's keys some turns ahead into L2: one 128-byte line a lane and row half
+    auto ahead = [&](int s) {
+        const int row = min(s + (lane >> 1), s1 - 1), half = (lane & 1) * 64;
+        if (s < s1 && half < D) asm volatile("prefetch.global.L2 [%0];" ::"l"(kc + (size_t)row * D + half));
+        if (s < s1 && half < DV) asm volatile("prefetch.global.L2 [%0];" ::"l"(vc + (size_t)row * DV + half));
+    };
+
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // of heads 2t, 2t+1 (l: this lane's keys)
     float o[OT][4];
 #pragma unroll
@@ -267,6 +274,8 @@ window_decode_mma(const __grid_constant__ WindowArgs a, int chunks)
     if (s < s1) {
         load_k(s);
         load_v(s);
+#pragma unroll
+        for (int i = 1; i < kAhead; ++i) ahead(s + i * kMmaWarps * 16);
     }
     uint4 qr[KS];
 #pragma unroll
@@ -277,6 +286,7 @@ window_decode_mma(const __grid_constant__ WindowArgs a, int chunks)
     }
     for (; s < s1; s += kMmaWarps * 16) {
         const int next = s + kMmaWarps * 16;
+        ahead(s + kAhead * kMmaWarps * 16);
         float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int x = 0; x < KS; ++x) {
@@ -395,12 +405,9 @@ window_decode_mma(const __grid_constant__ WindowArgs a, int chunks)
 
 // One launch: clusters of `splits` CTAs share a (sequence, kv head, head chunk).
 template <typename F>
-cudaError_t launch_clusters(F kern, const WindowArgs& a, int heads, int threads, int least)
+cudaError_t launch_clusters(F kern, const WindowArgs& a, int heads, int threads, int splits)
 {
-    const int group = a.Hq / a.Hkv, chunks = (group + heads - 1) / heads;
-    const long long units = (long long)a.B * a.Hkv * chunks;
-    int splits = 1;
-    while (splits < kMaxSplit && units * splits < 148 * 4 && (a.window + a.sinks) / (splits * 2) >= least) splits *= 2;
+    const int chunks = (a.Hq / a.Hkv + heads - 1) / heads;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(splits, a.Hkv * chunks, a.B);
     cfg.blockDim = dim3(threads);
@@ -414,11 +421,28 @@ cudaError_t launch_clusters(F kern, const WindowArgs& a, int heads, int threads,
     return cudaLaunchKernelEx(&cfg, kern, a, chunks);
 }
 
+// CTAs a (sequence, kv head, head chunk): enough for `want` in all, each with at least `least` slots.
+int splits_for(const WindowArgs& a, int heads, int want, int least, int most)
+{
+    const int chunks = (a.Hq / a.Hkv + heads - 1) / heads;
+    const long long units = (long long)a.B * a.Hkv * chunks;
+    int splits = 1;
+    while (splits < most && units * splits < want && (a.window + a.sinks) / (splits * 2) >= least) splits *= 2;
+    return splits;
+}
+
 template <int D, int DV>
 cudaError_t launch_dd(const WindowArgs& a)
 {
-    if (a.dtype == LA_BF16) return launch_clusters(window_decode_mma<D, DV>, a, kMmaHeads, kMmaWarps * 32, 64);
-    return launch_clusters(window_decode_simt<float, D, DV>, a, kHeads, kThreads, 64);
+    if (a.dtype == LA_BF16) {
+        // few sequences: eight warps a CTA halve the serial walk of a warp; many: four warps and three CTAs an SM
+        const int wide = splits_for(a, kMmaHeads, 148, 128, kMaxSplit);
+        const int chunks = (a.Hq / a.Hkv + kMmaHeads - 1) / kMmaHeads;
+        if ((long long)a.B * a.Hkv * chunks * wide <= 148)
+            return launch_clusters(window_decode_mma<D, DV, 8>, a, kMmaHeads, 256, wide);
+        return launch_clusters(window_decode_mma<D, DV, 4>, a, kMmaHeads, 128, splits_for(a, kMmaHeads, 148 * 4, 64, 8));
+    }
+    return launch_clusters(window_decode_simt<float, D, DV>, a, kHeads, kThreads, splits_for(a, kHeads, 148 * 4, 64, 8));
 }
 
 }  // namespace
