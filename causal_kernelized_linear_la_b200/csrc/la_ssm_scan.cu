@@ -23,6 +23,7 @@
 // its end state and sum of dt; since the decay over a segment is
 // exp(A sum dt), each segment of the second kernel folds the segments before
 // it into its own start state and runs once more with outputs.
+#include "f32x2.cuh"
 #include "la_internal.cuh"
 #include "sm100.cuh"
 
@@ -42,33 +43,6 @@ struct Lens {
     int use;
     int n[kMaxSeqLens];
 };
-
-// Two fp32 values in one register pair, for the packed arithmetic of sm_100.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pack2(float a, float b)
-{
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2(f2 v)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b)
-{
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
-{
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 
 // log(1 + e^v) = max(v, 0) + log1p(e), e = e^-|v| in (0, 1], and log1p(e) =
 // 2 atanh(r) with r = e / (2 + e) <= 1/3: the odd series of atanh to r^13 is

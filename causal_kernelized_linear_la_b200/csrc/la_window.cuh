@@ -153,12 +153,13 @@ struct KeyWalk {
         const Span t = turn_slots(qb - 1), p = past_slots(qb - 1);             // the last query sees the least
         return e <= sink_slots().hi || (b >= t.lo && e <= t.hi) || (b >= p.lo && e <= p.hi);
     }
-    // keys of tile it, counted from its base, that hold a token: the rest may hold anything
-    __device__ __forceinline__ int live(int it) const
+    // cache slots in use: always a prefix of them
+    __device__ __forceinline__ int held() const
     {
-        const int held = start < sinks ? start : sinks + (taken < window ? taken : window);
-        return (is_cache(it) ? held : len) - base(it);
+        return start < sinks ? start : sinks + (taken < window ? taken : window);
     }
+    // keys of tile it, counted from its base, that hold a token: the rest may hold anything
+    __device__ __forceinline__ int live(int it) const { return (is_cache(it) ? held() : len) - base(it); }
     // 32 keys from `key` on (a slot or a new token): bit c is set if query i sees key + c
     __device__ __forceinline__ static uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
     __device__ __forceinline__ static uint32_t within(Span s, int key) { return below(s.hi - key) & ~below(s.lo - key); }

@@ -9,23 +9,31 @@
 // A CTA takes 256 queries of one head as two tiles of 128 (the M of an MMA)
 // and walks the key tiles of 128 that any of them sees: cache slots, the
 // prompt's own sinks, the window's band (KeyWalk).  The two tiles alternate on
-// the tensor pipe: while one warpgroup turns its scores into weights (one
+// the tensor pipe: while one tile's warps turn its scores into weights (one
 // thread a query, the row in registers), the pipe runs the other tile's
 // products.  Weights go back to TMEM as bf16, over the scores they came from,
-// and are the A operand of P V from there.
+// and are the A operand of P V from there, 64 keys at a time.
 //   warps 0-3, 4-7  softmax of tile 0, 1; rescale; output
 //   warp 8          TMA: Q once, then K and V tiles through a ring
-//   warp 9          MMA issue
+//   warp 9          MMA issue; describes each key tile to the softmax warps
 //   warp 10         zeroes the value rows of a tile that hold no token: padding
 //                   and unfilled slots may hold NaN, and 0 * NaN is not 0
 // The weights are rounded to bf16 (half a step, 2^-8): the tensor cores take
 // both operands of a product in one type.  l adds the weights before that
 // rounding, in fp32.
 //
-// Bound: per 128 x 128 tile, 2 MMAs of 128 x 128 x d and 16384 exponentials,
-// which at d = 128 take the tensor pipe and the SFU about equally long.
+// Bound: per 128 x 128 tile, 2 products of 128 x 128 x d (at d = 128 16
+// instructions of 64 clocks) and 16384 exponentials (1024 clocks of the SFU).  A pair
+// of tiles takes about 3700 clocks where the pipe needs 2060: a tile's own chain
+// (load of the scores 350, maximum 250, exponentials 1100 and more while the
+// other tile uses the SFU too, products 1024, hand-offs) is longer than what the
+// other tile hides.  A 16384-token prompt (32 heads of 128, window 4096) runs at
+// 950 to 1090 TFLOP/s, at the card's 1000 W limit.  Measured and not kept: two
+// threads a query (1021 against 1014 us), an issuing warp a tile (1012), a
+// quarter of the exponentials as polynomials on the FMA pipe (1033 to 1180).
 #include <cudaTypedefs.h>
 
+#include "f32x2.cuh"
 #include "la_window.cuh"
 #include "sm100.cuh"
 
@@ -49,9 +57,10 @@ struct Plan {
     static constexpr int STAGE = KB > VB ? KB : VB;
     static constexpr int OFF_RING = 2 * QB;
     static constexpr int OFF_BAR = OFF_RING + STAGES * STAGE;
-    // full[S] empty[S] q_full s_full[2] p_full[2] o_done[2] clean[3] drain
-    static constexpr int NBAR = 2 * STAGES + 11;
-    static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
+    // full[S] empty[S] q_full s_full[2] p_full[2][2] o_done[2] clean[3] drain
+    static constexpr int NBAR = 2 * STAGES + 13;
+    static constexpr int OFF_DESC = OFF_BAR + NBAR * 8;           // [2] int2: the key tile behind each tile's scores
+    static constexpr int OFF_TMEM = OFF_DESC + 16;
     static constexpr int BYTES = OFF_TMEM + 16 + 1024;
     static_assert(BYTES <= 232448, "shared memory plan exceeds the per-block limit");
     // TMEM columns: scores (and weights) of both tiles, outputs of both tiles
@@ -87,6 +96,25 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t on;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(on));
+    return on != 0;
+}
+
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
 {
     uint32_t r[32];
@@ -112,6 +140,8 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[1
         : "memory");
 }
 
+enum TileFlags : int { kMasked = 1, kCacheTile = 2, kLastTile = 4 };
+
 // grid: (heads, pairs of query tiles, sequences)
 template <int D, int DV>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -119,10 +149,13 @@ window_prefill_tc(const __grid_constant__ Maps maps, const __grid_constant__ Win
                   const __grid_constant__ WindowLens lens)
 {
     using P = Plan<D, DV>;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // warp number and start come through a shuffle: the compiler then knows them to be the same in
+    // every lane, and the issuing warp's descriptors and branches stay in the uniform registers that
+    // tcgen05.mma takes them from (moving them there per instruction halved the issue rate)
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
     const int b = blockIdx.z, h = blockIdx.x, kvh = h / (a.Hq / a.Hkv);
     const int len = lens.use ? lens.n[b] : a.N;
-    const int start = a.pos ? a.pos[b] : 0;
+    const int start = __shfl_sync(~0u, a.pos ? a.pos[b] : 0, 0);
     // later queries see at least as many keys: the longest walks start first
     const int q0 = ((int)gridDim.y - 1 - (int)blockIdx.y) * 2 * kM;
     if (start < 0 || q0 >= len) return;
@@ -133,7 +166,29 @@ window_prefill_tc(const __grid_constant__ Maps maps, const __grid_constant__ Win
     // tile g's queries [qa(g), qb(g)); tile 1 may be empty
     auto qa = [&](int g) { return q0 + g * kM; };
     auto qb = [&](int g) { return min(len, q0 + (g + 1) * kM); };
-    auto active = [&](int it, int g) { return qa(g) < len && w.any(it, qa(g), qb(g)); };
+    // Which band tiles (by their number, first key / kKeys) a query tile sees,
+    // and which it sees whole: ranges, so that the walk costs a few compares a
+    // tile.  A tile of sinks is seen from anywhere behind it.
+    int see0[2], see1[2], whole0[2], whole1[2];
+    const int sink_any = (w.sinks_left() + kKeys - 1) / kKeys, sink_all = w.sinks_left() / kKeys;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        see0[g] = max(0, qa(g) - w.window + 1) / kKeys;
+        see1[g] = qa(g) < len ? (qb(g) + kKeys - 1) / kKeys : 0;
+        whole0[g] = (max(0, qb(g) - w.window) + kKeys - 1) / kKeys;
+        whole1[g] = min(qa(g) + 1, len) / kKeys;
+    }
+    const int band_at = w.cache_tiles + w.sink_tiles;     // the walk's first band tile
+    auto active = [&](int it, int g) {
+        if (it < band_at) return qa(g) < len && w.any(it, qa(g), qb(g));
+        const int n = w.band0 + it - band_at;
+        return n < see1[g] && (n >= see0[g] || n < sink_any);
+    };
+    auto masked = [&](int it, int g) {
+        if (it < band_at) return !w.all(it, qa(g), qb(g));
+        const int n = w.band0 + it - band_at;
+        return !(n < whole1[g] && (n >= whole0[g] || n < sink_all));
+    };
 
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = align1024(smem_raw);
@@ -141,43 +196,54 @@ window_prefill_tc(const __grid_constant__ Maps maps, const __grid_constant__ Win
     uint64_t* empty = full + P::STAGES;
     uint64_t* q_full = empty + P::STAGES;
     uint64_t* s_full = q_full + 1;     // [2] scores in TMEM
-    uint64_t* p_full = s_full + 2;     // [2] weights in TMEM, O rescaled
-    uint64_t* o_done = p_full + 2;     // [2] P V complete
+    uint64_t* p_full = s_full + 2;     // [2][2] weights of the first, the other 64 keys in TMEM, O rescaled
+    uint64_t* o_done = p_full + 4;     // [2] P V complete
     uint64_t* clean = o_done + 2;      // [3] dead rows of the value tile are zero: the ring holds parts of three
     uint64_t* drain = clean + 3;       //     value tiles at most, so a barrier's phases are waited for in turn
+    int2* desc = reinterpret_cast<int2*>(sm + P::OFF_DESC);    // [2] first key and TileFlags
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + P::OFF_TMEM);
 
-    if (tid == 0) {
-        for (int s = 0; s < P::STAGES; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-        }
-        mbar_init(q_full, 1);
-        for (int g = 0; g < 2; ++g) {
-            mbar_init(&s_full[g], 1);
-            mbar_init(&p_full[g], 4);
-            mbar_init(&o_done[g], 1);
-        }
-        for (int x = 0; x < 3; ++x) mbar_init(&clean[x], 1);
-        mbar_init(drain, 1);
-        fence_mbar_init();
-    }
-    if (warp == 0) tmem_alloc(tmem_slot, P::T_COLS);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tbase = *tmem_slot;
-
     if (warp == kSoftWarps) {
-        // ---------------- TMA ----------------
+        if (lane < 5) {
+            const CUtensorMap* m = lane == 0 ? &maps.q : lane == 1 ? &maps.k : lane == 2 ? &maps.v : lane == 3 ? &maps.kc : &maps.vc;
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+        }
         if (lane == 0) {
-            const uint64_t pol_q = policy_evict_first(), pol_kv = policy_evict_last();   // heads share K and V
+            for (int s = 0; s < P::STAGES; ++s) {
+                mbar_init(&full[s], 1);
+                mbar_init(&empty[s], 1);
+            }
+            mbar_init(q_full, 1);
+            for (int g = 0; g < 2; ++g) {
+                mbar_init(&s_full[g], 2);      // the product, and its tile's description
+                mbar_init(&p_full[2 * g], 4);
+                mbar_init(&p_full[2 * g + 1], 4);
+                mbar_init(&o_done[g], 1);
+            }
+            for (int x = 0; x < 3; ++x) mbar_init(&clean[x], 1);
+            mbar_init(drain, 1);
+            fence_mbar_init();
+            // Q is on its way before the block's set-up is done
+            const uint64_t pol_q = policy_evict_first();
             const int nq = qa(1) < len ? 2 : 1;
             mbar_expect_tx(q_full, nq * P::QB);
             for (int g = 0; g < nq; ++g)
                 for (int x = 0; x < D / 64; ++x)
                     tma_load_4d(sm + g * P::QB + x * (kM * 128), &maps.q, x * 64, qa(g), h * maps.qh, b * maps.qb, q_full,
                                 pol_q);
+        }
+        __syncwarp();
+    }
+    if (warp == 0) tmem_alloc(tmem_slot, P::T_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = __shfl_sync(~0u, *tmem_slot, 0);
+
+    if (warp == kSoftWarps) {
+        // ---------------- TMA ----------------
+        if (lane == 0) {
+            const uint64_t pol_kv = policy_evict_last();   // heads share K and V
             int item = 0;
             bool ok = true;
             for (int it = 0; it < tiles && ok; ++it) {
@@ -203,68 +269,111 @@ window_prefill_tc(const __grid_constant__ Maps maps, const __grid_constant__ Win
         }
     } else if (warp == kSoftWarps + 1) {
         // ---------------- MMA issue ----------------
-        if (lane == 0) {
-            const uint32_t id_s = idesc_bf16_f32(kM, kKeys, 0, 0), id_o = idesc_bf16_f32(kM, DV, 0, 1);
-            uint64_t dq[2];
-            for (int g = 0; g < 2; ++g) dq[g] = sdesc_sw128(smem_u32(sm + g * P::QB), 16, 1024);
-            auto scores = [&](int g, int item) {      // S_g = Q_g K^T
-                const uint64_t dk = sdesc_sw128(smem_u32(sm + P::OFF_RING + (item % P::STAGES) * P::STAGE), 16, 1024);
+        // The whole warp walks the tiles; one elected lane issues.  A wait that
+        // gave up makes the later ones return at once: what is issued then
+        // works on stale operands inside the CTA's own memory, and the error
+        // word is set.
+        const bool leader = elect_one();
+        bool dead = false;
+        auto wait = [&](uint64_t* bar, int phase, unsigned int site) {
+            if (!dead) dead = !mbar_wait(bar, phase & 1, site);
+            __syncwarp();
+        };
+        // a negative scale negates Q (the descriptor's bit 13), so the maximum of the scores is what counts
+        const uint32_t id_s = idesc_bf16_f32(kM, kKeys, 0, 0) | (a.scale < 0.f ? 1u << 13 : 0u), id_o = idesc_bf16_f32(kM, DV, 0, 1);
+        const uint32_t q_at = smem_u32(sm), ring_at = q_at + P::OFF_RING;
+        // a key tile to visit: its number, and per query tile whether and how
+        struct Tile {
+            int it, base;
+            bool on[2];
+            int flags[2];
+        };
+        auto next_tile = [&](int from) {
+            Tile t{from, 0, {false, false}, {0, 0}};
+            for (; t.it < tiles; ++t.it) {
+                t.on[0] = active(t.it, 0);
+                t.on[1] = active(t.it, 1);
+                if (t.on[0] || t.on[1]) break;
+            }
+            if (t.it < tiles) {
+                const bool old = w.is_cache(t.it);
+                t.base = w.base(t.it);
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                    // the tile of a query tile's last key is its last: keys behind it are in the future
+                    t.flags[g] = (masked(t.it, g) ? kMasked : 0) | (old ? kCacheTile : 0) |
+                                 (!old && t.base + kKeys >= qb(g) ? kLastTile : 0);
+            }
+            return t;
+        };
+        auto scores = [&](int g, const Tile& t, int item) {      // S_g = Q_g K^T
+            const uint64_t dq = sdesc_sw128(q_at + g * P::QB, 16, 1024);
+            const uint64_t dk = sdesc_sw128(ring_at + (item % P::STAGES) * P::STAGE, 16, 1024);
+            if (leader) {
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint32_t off = ((ks / 4) * (kKeys * 128) + (ks % 4) * 32) >> 4;
-                    mma_bf16(tbase + P::T_S + g * kKeys, dq[g] + off, dk + off, id_s, ks > 0);
+                    mma_bf16(tbase + P::T_S + g * kKeys, dq + off, dk + off, id_s, ks > 0);
                 }
                 mma_commit(&s_full[g]);
-            };
-            auto loaded = [&](int item) {
-                return mbar_wait(&full[item % P::STAGES], (item / P::STAGES) & 1, kErrTmaLoad);
-            };
-            int it = 0;
-            auto next_tile = [&](int from) {
-                int t = from;
-                while (t < tiles && !active(t, 0) && !active(t, 1)) ++t;
-                return t;
-            };
-            it = next_tile(0);
-            int done[2] = {0, 0}, item = 0, nv = 0;
-            bool ok = mbar_wait(q_full, 0, kErrTmaLoad) && loaded(0);
-            tc_fence_after();
-            if (ok) {
-                for (int g = 0; g < 2; ++g)
-                    if (active(it, g)) scores(g, 0);
-                mma_commit(&empty[0]);
+                desc[g] = make_int2(t.base, t.flags[g]);
+                mbar_arrive(&s_full[g]);
             }
-            while (ok && it < tiles) {
-                const int nx = next_tile(it + 1);
-                const int vi = item + 1, ki = item + 2;    // ring items: V of this tile, K of the next
-                const uint64_t dv = sdesc_sw128(smem_u32(sm + P::OFF_RING + (vi % P::STAGES) * P::STAGE), kKeys * 128, 1024);
-                ok = loaded(vi) && mbar_wait(&clean[nv % 3], (nv / 3) & 1, kErrMma);
-                ++nv;
-                if (ok && nx < tiles) ok = loaded(ki);
-                for (int g = 0; g < 2 && ok; ++g) {
-                    if (active(it, g)) {
-                        // O_g += P_g V
-                        ok = mbar_wait(&p_full[g], done[g] & 1, kErrMma);
-                        if (!ok) break;
-                        tc_fence_after();
+            __syncwarp();
+        };
+        auto loaded = [&](int item) { wait(&full[item % P::STAGES], item / P::STAGES, kErrTmaLoad); };
+        auto release = [&](int item) {
+            if (leader) mma_commit(&empty[item % P::STAGES]);
+            __syncwarp();
+        };
+        Tile cur = next_tile(0);
+        int done[2] = {0, 0}, item = 0, nv = 0;
+        wait(q_full, 0, kErrTmaLoad);
+        loaded(0);
+        tc_fence_after();
 #pragma unroll
-                        for (int ks = 0; ks < kKeys / 16; ++ks)
-                            mma_bf16_ts(tbase + P::T_O + g * DV, tbase + P::T_S + g * kKeys + ks * 8,
-                                        dv + ((ks * 2048) >> 4), id_o, done[g] > 0 || ks > 0);
-                        mma_commit(&o_done[g]);
-                        ++done[g];
+        for (int g = 0; g < 2; ++g)
+            if (cur.on[g]) scores(g, cur, 0);
+        release(0);
+        while (cur.it < tiles) {
+            const Tile nx = next_tile(cur.it + 1);
+            const bool more = nx.it < tiles;
+            const int vi = item + 1, ki = item + 2;    // ring items: V of this tile, K of the next
+            const uint64_t dv = sdesc_sw128(ring_at + (vi % P::STAGES) * P::STAGE, kKeys * 128, 1024);
+            loaded(vi);
+            wait(&clean[nv % 3], nv / 3, kErrMma);
+            ++nv;
+            if (more) loaded(ki);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (cur.on[g]) {
+                    // O_g += P_g V, 64 keys at a time
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        wait(&p_full[2 * g + half], done[g], kErrMma);
+                        tc_fence_after();
+                        if (leader) {
+#pragma unroll
+                            for (int ks = half * 4; ks < half * 4 + 4; ++ks)
+                                mma_bf16_ts(tbase + P::T_O + g * DV, tbase + P::T_S + g * kKeys + ks * 8,
+                                            dv + ((ks * 2048) >> 4), id_o, done[g] > 0 || ks > 0);
+                            if (half) mma_commit(&o_done[g]);
+                        }
+                        __syncwarp();
                     }
-                    if (nx < tiles && active(nx, g)) scores(g, ki);
+                    ++done[g];
                 }
-                mma_commit(&empty[vi % P::STAGES]);
-                if (nx < tiles) mma_commit(&empty[ki % P::STAGES]);
-                it = nx;
-                item += 2;
+                if (more && nx.on[g]) scores(g, nx, ki);
             }
-            // nothing in flight before TMEM is released
-            mma_commit(drain);
-            mbar_wait(drain, 0, kErrMma);
+            release(vi);
+            if (more) release(ki);
+            cur = nx;
+            item += 2;
         }
+        // nothing in flight before TMEM is released
+        if (leader) mma_commit(drain);
+        __syncwarp();
+        mbar_wait(drain, 0, kErrMma);
     } else if (warp == kSoftWarps + 2) {
         // ---------------- dead value rows ----------------
         bool ok = true;
@@ -293,49 +402,42 @@ window_prefill_tc(const __grid_constant__ Maps maps, const __grid_constant__ Win
         // ---------------- softmax ----------------
         const int g = warp >> 2, quad = warp & 3;
         const int row = qa(g) + quad * 32 + lane;
-        const bool flip = a.scale < 0.f;
         // a zero scale weighs every visible key the same; it keeps masked keys at -inf
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
         const float slack = kSlack / c;
-        float m = -INFINITY, l0 = 0.f, l1 = 0.f;
+        float m = -INFINITY;
+        f2 l[2] = {0, 0};    // sums of the weights of four classes of keys
         const uint32_t ts = tmem_addr(tbase, quad, P::T_S + g * kKeys), to = tmem_addr(tbase, quad, P::T_O + g * DV);
         int n = 0;          // tiles done
         bool ok = true;
-        for (int it = 0; it < tiles; ++it) {
-            if (!active(it, g)) continue;
+        for (bool last = false; !last; ++n) {
             if (!mbar_wait(&s_full[g], n & 1, kErrMma)) { ok = false; break; }
             tc_fence_after();
+            const int2 tile = desc[g];
+            last = tile.y & kLastTile;
             float s[4][32];
 #pragma unroll
             for (int x = 0; x < 4; ++x) tmem_ld32(ts + x * 32, s[x]);
             tmem_ld_wait();
 #pragma unroll
             for (int x = 0; x < 4; ++x) tmem_regs_after_wait(s[x]);
-            if (flip) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) s[x][j] = -s[x][j];
-            }
-            if (!w.all(it, qa(g), qb(g))) {
-                const bool old = w.is_cache(it);
-                const int key = w.base(it);
+            if (tile.y & kMasked) {
+                const bool old = tile.y & kCacheTile;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const uint32_t see = w.bits(old, row, key + x * 32);
+                    const uint32_t see = w.bits(old, row, tile.x + x * 32);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) s[x][j] = (see >> j) & 1u ? s[x][j] : -INFINITY;
                 }
             }
-            float t0 = s[0][0], t1 = s[1][0], t2 = s[2][0], t3 = s[3][0];
+            float t[4];
 #pragma unroll
-            for (int j = 1; j < 32; ++j) {
-                t0 = fmaxf(t0, s[0][j]);
-                t1 = fmaxf(t1, s[1][j]);
-                t2 = fmaxf(t2, s[2][j]);
-                t3 = fmaxf(t3, s[3][j]);
+            for (int x = 0; x < 4; ++x) {
+                t[x] = fmaxf(s[x][0], s[x][1]);
+#pragma unroll
+                for (int j = 2; j < 32; j += 2) t[x] = max3(t[x], s[x][j], s[x][j + 1]);
             }
-            const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+            const float top = fmaxf(max3(t[0], t[1], t[2]), t[3]);
             const bool need = top > m + slack;       // also the first visible key: m = -inf
             if (__any_sync(~0u, need)) {
                 const bool had = m != -INFINITY;
@@ -355,32 +457,37 @@ window_prefill_tc(const __grid_constant__ Maps maps, const __grid_constant__ Win
                         tmem_st16(to + x, o);
                     }
                 }
-                l0 *= f;
-                l1 *= f;
+                l[0] = mul2(l[0], pack2(f, f));
+                l[1] = mul2(l[1], pack2(f, f));
                 if (need) m = top;
             }
             const float off = m == -INFINITY ? 0.f : -m * c;
+            const f2 c2 = pack2(c, c), off2 = pack2(off, off);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 uint32_t p[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const float e0 = ex2_approx(fmaf(s[x][2 * j], c, off)), e1 = ex2_approx(fmaf(s[x][2 * j + 1], c, off));
-                    l0 += e0;
-                    l1 += e1;
-                    p[j] = pack_bf16x2(e0, e1);
+                    const f2 y = fma2(pack2(s[x][2 * j], s[x][2 * j + 1]), c2, off2);
+                    const float2 yv = unpack2(y);
+                    const f2 e = pack2(ex2_approx(yv.x), ex2_approx(yv.y));
+                    l[j % 2] = add2(l[j % 2], e);
+                    const float2 v = unpack2(e);
+                    p[j] = pack_bf16x2(v.x, v.y);
                 }
                 tmem_st16u(ts + x * 16, p);
+                if (x % 2 == 1) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * g + x / 2]);
+                }
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[g]);
-            ++n;
         }
         if (ok && mbar_wait(&o_done[g], (n - 1) & 1, kErrMma)) {
             tc_fence_after();
-            const float inv = 1.f / (l0 + l1);     // every query sees itself
+            const float2 l1 = unpack2(add2(l[0], l[1]));
+            const float inv = 1.f / (l1.x + l1.y);     // every query sees itself
             __nv_bfloat16* op = (__nv_bfloat16*)a.out + b * a.st.out_batch + h * a.st.out_head + row * a.st.out_row;
 #pragma unroll 1
             for (int x = 0; x < DV; x += 32) {
