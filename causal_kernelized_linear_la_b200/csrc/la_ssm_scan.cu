@@ -84,15 +84,36 @@ __device__ __forceinline__ void bar_arrive(uint32_t id, uint32_t count)
 template <typename T, int ROWS, int PITCH, int BYTES>
 __device__ __forceinline__ void load_pieces(T* dst, const T* src, long long row_stride, int rows, int cols, int tid)
 {
-    constexpr int PER = BYTES / (int)sizeof(T), N = PITCH / PER;
-#pragma unroll 4
-    for (int e = tid; e < ROWS * N; e += kPrep) {
-        const int t = e / N, c = (e % N) * PER;
-        const int left = t < rows ? min(PER, max(0, cols - c)) : 0;
-        const T* s = left > 0 ? src + t * row_stride + c : src;
-        T* d = dst + t * PITCH + c;
-        if (BYTES == 4) cp_async4(d, s, left * sizeof(T));
-        else *d = left > 0 ? *s : from_f32<T>(0.f);
+    constexpr int PER = BYTES / (int)sizeof(T), N = PITCH / PER, STEP = kPrep / N;   // pieces of a row, rows of a pass
+    static_assert(kPrep % N == 0 && ROWS % STEP == 0, "a thread keeps its columns");
+    const int c = tid % N * PER, t0 = tid / N;
+    const int left = min(PER, max(0, cols - c));
+    const T* s = src + (left > 0 ? t0 * row_stride + c : 0);
+    const long long step = left > 0 ? STEP * row_stride : 0;
+    T* d = dst + t0 * PITCH + c;
+    if (BYTES == 4) {
+        if (rows >= ROWS) {
+#pragma unroll
+            for (int i = 0; i < ROWS / STEP; ++i, s += step) cp_async4(d + i * STEP * PITCH, s, left * sizeof(T));
+        } else {
+#pragma unroll
+            for (int i = 0; i < ROWS / STEP; ++i, s += step) {
+                const bool on = t0 + i * STEP < rows;
+                cp_async4(d + i * STEP * PITCH, on ? s : src, on ? left * sizeof(T) : 0);
+            }
+        }
+    } else {
+        // the element itself through registers, eight loads at a time
+#pragma unroll
+        for (int i0 = 0; i0 < ROWS / STEP; i0 += 8) {
+            T v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i, s += step)
+                v[i] = i0 + i < ROWS / STEP && left > 0 && t0 + (i0 + i) * STEP < rows ? *s : from_f32<T>(0.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i0 + i < ROWS / STEP) d[(i0 + i) * STEP * PITCH] = v[i];
+        }
     }
 }
 
