@@ -1,5 +1,7 @@
 // Packed fp32 arithmetic of sm_100: two values in one register pair.  A packed
 // instruction takes the pipe as long as two scalar ones but one issue slot.
+// And the SFU's reciprocal and SiLU without the range handling of the
+// compiler's own forms, which costs more instructions than they do.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -37,6 +39,22 @@ __device__ __forceinline__ f2 add2(f2 a, f2 b)
     f2 r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+
+// 1 / x for x in [1, inf] (1 / inf = 0): one SFU instruction, relative error 2^-23
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// y / (1 + e^-y), with e^-y as 2^(-y log2 e) flushed to zero where it is subnormal
+__device__ __forceinline__ float silu_approx(float y)
+{
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y * -1.4426950408889634f));
+    return y * rcp_approx(1.f + e);
 }
 
 }  // namespace sm100

@@ -263,7 +263,8 @@ la_status check_window(WindowArgs* w, const void* q, const void* k, const void* 
     if (cfg->dtype != LA_F32 && cfg->dtype != LA_BF16) return LA_ERR_INVALID;
     if (!head_ok(d) || !head_ok(dv)) return LA_ERR_UNSUPPORTED;
     constexpr int kTop = (1 << 30) - 1;   // row and slot numbers add up inside 32 bits
-    if (N > kTop || (k_cache && (long long)window + sinks > kTop)) return LA_ERR_UNSUPPORTED;
+    constexpr int kMostTokens = 65535 * 256;   // query tiles of one launch
+    if (N > kMostTokens || (k_cache && (long long)window + sinks > kTop)) return LA_ERR_UNSUPPORTED;
     if (window > kTop) window = kTop;     // without a cache: more than any prompt reaches back
     if (sinks > kTop) sinks = kTop;
     if (Hq > 0 && (Hkv == 0 || Hq % Hkv != 0)) return LA_ERR_INVALID;

@@ -19,10 +19,13 @@
 // alternate, so that four to eight 16-byte loads of a thread are always in
 // flight.  One token a sequence: a thread takes several sequences, so that the
 // filter, larger than a token's rows, is loaded once for them.
+#include "f32x2.cuh"
 #include "la_internal.cuh"
 
 namespace la {
 namespace {
+
+using namespace sm100;
 
 constexpr int kThreads = 256;
 constexpr int kHalf = 4;    // rows of a half-batch
@@ -69,7 +72,7 @@ __device__ __forceinline__ void row_store(T* p, const float (&f)[V])
 // fp32 outputs take the accurate exponential; bf16 rounding hides the fast one's error
 template <typename T> __device__ __forceinline__ float silu(float y);
 template <> __device__ __forceinline__ float silu<float>(float y) { return y / (1.f + expf(-y)); }
-template <> __device__ __forceinline__ float silu<__nv_bfloat16>(float y) { return __fdividef(y, 1.f + __expf(-y)); }
+template <> __device__ __forceinline__ float silu<__nv_bfloat16>(float y) { return silu_approx(y); }
 
 // V channels' filters [V][W] and biases
 template <int W, int V>
@@ -132,27 +135,35 @@ ssm_conv_kernel(const T* __restrict__ x, const float* __restrict__ weight, const
             for (int u = 0; u < kHalf; ++u) rows[a][u] = fetch(t0 + HIST + a * kHalf + u);
         float wt[W][V], b0[V];
         load_filter<W, V>(weight, bias, c0, wt, b0);
-        // acc[k]: the output k tokens ahead of the next row
-        float acc[W][V];
+        // pairs of channels go through packed FMAs: half the issue slots
+        constexpr int VP = (V + 1) / 2;
+        f2 w2[W][VP], b2[VP], acc[W][VP];      // acc[k]: the output k tokens ahead of the next row
 #pragma unroll
-        for (int k = 0; k < W; ++k)
+        for (int j = 0; j < VP; ++j) {
+            b2[j] = pack2(b0[2 * j], V > 1 ? b0[2 * j + (V > 1)] : 0.f);
 #pragma unroll
-            for (int j = 0; j < V; ++j) acc[k][j] = b0[j];
+            for (int k = 0; k < W; ++k) {
+                w2[k][j] = pack2(wt[k][2 * j], V > 1 ? wt[k][2 * j + (V > 1)] : 0.f);
+                acc[k][j] = b2[j];
+            }
+        }
         auto add = [&](const Row<T, V>& row) {
             float f[V];
             row_f32<T, V>(row, f);
 #pragma unroll
-            for (int k = 0; k < W; ++k)
+            for (int j = 0; j < VP; ++j) {
+                const f2 x2 = pack2(f[2 * j], V > 1 ? f[2 * j + (V > 1)] : 0.f);
 #pragma unroll
-                for (int j = 0; j < V; ++j) acc[k][j] = fmaf(wt[W - 1 - k][j], f[j], acc[k][j]);
+                for (int k = 0; k < W; ++k) acc[k][j] = fma2(w2[W - 1 - k][j], x2, acc[k][j]);
+            }
         };
         auto shift = [&]() {
 #pragma unroll
-            for (int k = 0; k + 1 < W; ++k)
+            for (int j = 0; j < VP; ++j) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) acc[k][j] = acc[k + 1][j];
-#pragma unroll
-            for (int j = 0; j < V; ++j) acc[W - 1][j] = b0[j];
+                for (int k = 0; k + 1 < W; ++k) acc[k][j] = acc[k + 1][j];
+                acc[W - 1][j] = b2[j];
+            }
         };
         // the history: row t0 + i is tap i of the first output (acc[0] after HIST shifts)
 #pragma unroll
@@ -169,7 +180,11 @@ ssm_conv_kernel(const T* __restrict__ x, const float* __restrict__ weight, const
                     add(rows[a][u]);
                     float out[V];
 #pragma unroll
-                    for (int j = 0; j < V; ++j) out[j] = act ? silu<T>(acc[0][j]) : acc[0][j];
+                    for (int j = 0; j < V; ++j) {
+                        const float2 q = unpack2(acc[0][j / 2]);
+                        const float y1 = j % 2 ? q.y : q.x;
+                        out[j] = act ? silu<T>(y1) : y1;
+                    }
                     if (t + a * kHalf + u < t1) row_store<T, V>(yp, out);
                     yp += D;
                     shift();

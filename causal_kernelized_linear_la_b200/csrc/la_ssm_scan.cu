@@ -50,7 +50,7 @@ struct Lens {
 __device__ __forceinline__ float softplus(float v)
 {
     const float e = ex2_approx(-fabsf(v) * kLog2e);
-    const float r = __fdividef(e, 2.f + e), q = r * r;
+    const float r = e * rcp_approx(2.f + e), q = r * r;
     float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
     p = fmaf(p, q, 1.f / 9.f);
     p = fmaf(p, q, 1.f / 7.f);
@@ -61,7 +61,7 @@ __device__ __forceinline__ float softplus(float v)
 }
 template <typename T> __device__ __forceinline__ float silu(float v);
 template <> __device__ __forceinline__ float silu<float>(float v) { return v / (1.f + expf(-v)); }
-template <> __device__ __forceinline__ float silu<__nv_bfloat16>(float v) { return __fdividef(v, 1.f + __expf(-v)); }
+template <> __device__ __forceinline__ float silu<__nv_bfloat16>(float v) { return silu_approx(v); }
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, uint32_t src_bytes)
 {

@@ -415,8 +415,8 @@ LA_API la_status la_ssm_step(const void* x, const void* delta, const float* A, c
  * The calls do not change pos, and slots not yet filled never reach a result.
  *
  * Query head h reads kv head h / (Hq / Hkv); Hq is a multiple of Hkv.  d, dv in
- * {64, 128}; window >= 1, sinks >= 0; N < 2^30 and, with a cache, sinks +
- * window < 2^30 (LA_ERR_UNSUPPORTED); positions stay below 2^31; rows of one
+ * {64, 128}; window >= 1, sinks >= 0; N <= 65535 * 256 and, with a cache,
+ * sinks + window < 2^30 (LA_ERR_UNSUPPORTED); positions stay below 2^31; rows of one
  * head are at least d (dv) elements apart.  Sums, maxima and outputs accumulate in fp32.  All pointers are
  * 16-byte aligned, and so are the rows (strides are multiples of 16 bytes).
  */
@@ -444,8 +444,10 @@ typedef struct {
  *              they hold; padding rows of out are not written.
  *   cfg        dtype and stream are used.
  *
- * Inside a sequence, values of v are expected to be finite: a token that a
- * query does not see enters its sum with weight zero.
+ * Inside a sequence, v is expected to be finite: a token that a query does not
+ * see enters its sum with weight zero.  k may hold anything there.
+ * bf16 runs on the tensor cores and rounds the weights w_ij (relative to the
+ * row's running reference) to bf16; fp32 keeps fp32 arithmetic throughout.
  * LA_ERR_INVALID, LA_ERR_UNSUPPORTED, LA_ERR_ALIGN as elsewhere; LA_ERR_INVALID
  * too if out, or a cache, overlaps k or v.
  */

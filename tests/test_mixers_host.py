@@ -1,0 +1,195 @@
+"""State-space and sliding-window entry points: argument checks that return
+before any CUDA call, host-only queries, and the binding's own checks (no GPU
+needed; the pointers below are never dereferenced)."""
+import ctypes
+
+import pytest
+import torch
+
+import causal_kernelized_linear_la_b200 as la
+from causal_kernelized_linear_la_b200 import LaConfig, LaSsmStrides, LaWindowStrides
+
+P = 1 << 20
+C = ctypes.c_void_p
+
+
+def _cfg(dtype=la.LA_BF16, S0=None, ws=None, wsb=0):
+    return LaConfig(dtype, 0, 0.0, None, S0, None, ws, wsb)
+
+
+def _conv(x=P, w_=P, bias=None, cache=None, out=P, cache_out=None, lens=None, B=1, N=8, D=16, w=4, xb=128, xt=16, cfg=None):
+    arr = None if lens is None else (ctypes.c_int * len(lens))(*lens)
+    c = _cfg() if cfg is None else cfg
+    return la.lib().la_ssm_conv(C(x), C(w_), C(bias), C(cache), C(out), C(cache_out), arr, B, N, D, w, 1, xb, xt,
+                                ctypes.byref(c))
+
+
+def test_conv_refusals():
+    assert _conv(B=-1) == la.LA_ERR_INVALID
+    assert _conv(N=-1) == la.LA_ERR_INVALID
+    assert _conv(w=0) == la.LA_ERR_INVALID
+    assert _conv(w=9) == la.LA_ERR_UNSUPPORTED
+    assert _conv(xt=-1) == la.LA_ERR_INVALID
+    assert _conv(x=0) == la.LA_ERR_INVALID
+    assert _conv(out=0) == la.LA_ERR_INVALID
+    assert _conv(cfg=_cfg(dtype=5)) == la.LA_ERR_INVALID
+    assert _conv(lens=[9]) == la.LA_ERR_INVALID
+    assert _conv(lens=[-1]) == la.LA_ERR_INVALID
+    assert _conv(x=P + 1) == la.LA_ERR_ALIGN                       # off its elements
+    assert _conv(w_=P + 4) == la.LA_ERR_ALIGN
+    assert _conv(cache=P, cache_out=P + 16) == la.LA_ERR_INVALID   # overlaps the cache in part
+    assert _conv(cache_out=P + 32) == la.LA_ERR_INVALID            # overlaps x
+    # the last row of a strided x: 7 * 64 + 16 elements
+    assert _conv(xt=64, cache_out=P + 2 * (7 * 64 + 8)) == la.LA_ERR_INVALID
+    assert _conv(B=0) == la.LA_OK
+    assert _conv(D=0) == la.LA_OK
+    assert _conv(N=0, x=0, w_=0, out=0) == la.LA_OK                # no tokens and no cache to pass on
+
+
+def _scan(x=P, A=P, h_out=2 * P, lens=None, B=1, N=8, D=16, G=1, n=4, st=None, cfg=None, z=None, out=P):
+    arr = None if lens is None else (ctypes.c_int * len(lens))(*lens)
+    c = _cfg() if cfg is None else cfg
+    return la.lib().la_ssm_scan(C(x), C(P), C(A), C(P), C(P), None, C(z), None, C(out), C(h_out), arr, B, N, D, G, n, 1,
+                                None if st is None else ctypes.byref(st), ctypes.byref(c))
+
+
+def test_scan_refusals():
+    assert _scan(B=-1) == la.LA_ERR_INVALID
+    assert _scan(N=-1) == la.LA_ERR_INVALID
+    assert _scan(n=0) == la.LA_ERR_INVALID
+    assert _scan(n=65) == la.LA_ERR_UNSUPPORTED
+    assert _scan(G=3) == la.LA_ERR_INVALID                         # 16 channels in 3 groups
+    assert _scan(G=0) == la.LA_ERR_INVALID
+    assert _scan(x=0) == la.LA_ERR_INVALID
+    assert _scan(cfg=_cfg(dtype=3)) == la.LA_ERR_INVALID
+    assert _scan(A=P + 4) == la.LA_ERR_ALIGN
+    assert _scan(z=P + 1) == la.LA_ERR_ALIGN
+    assert _scan(h_out=2 * P + 8) == la.LA_ERR_ALIGN
+    assert _scan(lens=[9]) == la.LA_ERR_INVALID
+    assert _scan(st=LaSsmStrides(128, -16)) == la.LA_ERR_INVALID
+    assert _scan(cfg=_cfg(S0=2 * P)) == la.LA_ERR_INVALID          # final states over the start states
+    assert _scan(cfg=_cfg(S0=2 * P + 16)) == la.LA_ERR_INVALID
+    assert _scan(N=100000) == la.LA_ERR_WORKSPACE                  # few channels: several segments
+    assert _scan(B=0) == la.LA_OK
+    assert _scan(D=0, G=0) == la.LA_OK
+
+
+def test_scan_workspace():
+    ws = la.la_ssm_scan_workspace_bytes
+    assert ws(1, 8192, 4096, 1, 16) == 0                # enough channels for every SM: one segment
+    assert ws(1, 0, 512, 1, 16) == 0 and ws(0, 8, 512, 1, 16) == 0
+    assert ws(1, 64, 32, 1, 16) == 0                    # too short to cut
+    # one summary of 32 channels x (16 states + a sum) fp32 a segment and tile; whole tiles of
+    # 32 channels, so narrower layers take the same
+    n = ws(1, 32768, 512, 1, 16)
+    assert n > 0 and n % (16 * 32 * 17 * 4) == 0
+    assert ws(1, 32768, 500, 1, 16) == n
+    assert ws(2, 32768, 512, 1, 16) % (2 * 16 * 32 * 17 * 4) == 0
+    # the caller of a smaller batch never needs more than it was told
+    for N in (255, 256, 257, 4095, 32768, 100001):
+        assert ws(1, N, 40, 2, 5) % (2 * 32 * 9 * 4) == 0
+
+
+def _step(h=P, x=P, cfg=None, B=1, D=16, n=4, G=1):
+    c = _cfg() if cfg is None else cfg
+    return la.lib().la_ssm_step(C(x), C(P), C(P), C(P), C(P), None, None, None, C(h), C(P), B, D, G, n, 1, None,
+                                ctypes.byref(c))
+
+
+def test_step_refusals():
+    assert _step(h=0) == la.LA_ERR_INVALID
+    assert _step(h=P + 8) == la.LA_ERR_ALIGN
+    assert _step(n=65) == la.LA_ERR_UNSUPPORTED
+    assert _step(G=5) == la.LA_ERR_INVALID
+    assert _step(x=0) == la.LA_ERR_INVALID
+    assert _step(B=0, h=0) == la.LA_OK
+
+
+FAR = 1 << 40
+
+
+def _window(q=P, k=2 * P, v=3 * P, out=4 * P, kc=None, vc=None, pos=None, lens=None, B=1, Hq=2, Hkv=1, N=8, d=64, dv=64,
+            window=4, sinks=1, scale=0.1, st=None, cfg=None):
+    arr = None if lens is None else (ctypes.c_int * len(lens))(*lens)
+    c = _cfg() if cfg is None else cfg
+    return la.lib().la_window_prefill(C(q), C(k), C(v), C(out), C(kc), C(vc), C(pos), arr, B, Hq, Hkv, N, d, dv, window,
+                                      sinks, scale, None if st is None else ctypes.byref(st), ctypes.byref(c))
+
+
+def test_window_refusals():
+    bad, unsup, align = la.LA_ERR_INVALID, la.LA_ERR_UNSUPPORTED, la.LA_ERR_ALIGN
+    assert _window(B=-1) == bad
+    assert _window(window=0) == bad
+    assert _window(sinks=-1) == bad
+    assert _window(Hq=3, Hkv=2) == bad
+    assert _window(Hkv=0) == bad
+    assert _window(d=96) == unsup
+    assert _window(dv=32) == unsup
+    assert _window(N=65535 * 256 + 1) == unsup
+    assert _window(scale=float("nan")) == bad
+    assert _window(scale=float("inf")) == bad
+    assert _window(cfg=_cfg(dtype=9)) == bad
+    assert _window(q=0) == bad
+    assert _window(kc=FAR) == bad                               # half a cache
+    assert _window(pos=P) == bad                                # positions without a cache
+    assert _window(kc=FAR, vc=FAR + 64) == bad                  # the caches overlap
+    assert _window(kc=FAR, vc=2 * P) == bad                     # a cache over k
+    assert _window(kc=FAR, vc=FAR << 1, window=1 << 30) == unsup
+    assert _window(out=2 * P + 64) == bad                       # out over k
+    assert _window(q=P + 8) == align
+    assert _window(kc=FAR + 8, vc=FAR << 1) == align
+    assert _window(kc=FAR, vc=FAR << 1, pos=P + 2) == align
+    assert _window(lens=[9]) == bad
+    dense = [1024, 512, 64] * 4
+    assert _window(st=LaWindowStrides(*dense[:2], 68, *dense[3:])) == align     # rows off 16 bytes
+    assert _window(st=LaWindowStrides(*dense[:2], 32, *dense[3:])) == bad       # rows that share memory
+    assert _window(st=LaWindowStrides(-1024, *dense[1:])) == bad
+    assert _window(B=0) == la.LA_OK
+    assert _window(N=0, q=0, k=0, v=0, out=0) == la.LA_OK
+
+
+def test_decode_refusals():
+    def call(kc=FAR, vc=FAR << 1, pos=P, window=4, q=P):
+        c = _cfg()
+        return la.lib().la_window_decode_step(C(q), C(2 * P), C(3 * P), C(4 * P), C(kc), C(vc), C(pos), 1, 2, 1, 64, 64,
+                                              window, 1, 0.1, None, ctypes.byref(c))
+    assert call(kc=0, vc=0) == la.LA_ERR_INVALID
+    assert call(pos=0) == la.LA_ERR_INVALID
+    assert call(vc=0) == la.LA_ERR_INVALID
+    assert call(window=0) == la.LA_ERR_INVALID
+    assert call(q=P + 2) == la.LA_ERR_ALIGN
+
+
+def test_binding_checks():
+    x, w = torch.zeros(2, 8, 16), torch.zeros(16, 4)
+    with pytest.raises(ValueError, match="CUDA"):
+        la.la_ssm_conv(x, w)
+    with pytest.raises(ValueError, match="weight"):
+        la.la_ssm_conv(x, torch.zeros(15, 4))
+    with pytest.raises(ValueError, match="cache"):
+        la.la_ssm_conv(x, w, cache=torch.zeros(2, 4, 16))
+    with pytest.raises(ValueError, match="contiguous"):
+        la.la_ssm_conv(x.transpose(1, 2), torch.zeros(8, 4))
+    A, bc = torch.zeros(16, 4), torch.zeros(2, 8, 4)
+    with pytest.raises(ValueError, match="CUDA"):
+        la.la_ssm_scan(x, x, A, bc, bc)
+    with pytest.raises(ValueError, match="groups"):
+        la.la_ssm_scan(x, x, A, torch.zeros(2, 8, 3, 4), bc)
+    with pytest.raises(ValueError, match="C must"):
+        la.la_ssm_scan(x, x, A, bc, bc[:, :7])
+    with pytest.raises(ValueError, match="A must"):
+        la.la_ssm_scan(x, x, A[:, :3], bc, bc)
+    with pytest.raises(ValueError, match="dtype"):
+        la.la_ssm_scan(x, x.bfloat16(), A, bc, bc)
+    with pytest.raises(ValueError, match="h must"):
+        la.la_ssm_step(x[:, 0], x[:, 0], A, bc[:, 0], bc[:, 0], torch.zeros(2, 16, 5))
+    q, k = torch.zeros(1, 2, 8, 64), torch.zeros(1, 1, 8, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        la.la_window_prefill(q, k, k, 4)
+    with pytest.raises(ValueError, match="do not fit"):
+        la.la_window_prefill(q, k, k[:, :, :7], 4)
+    with pytest.raises(ValueError, match="k_cache"):
+        la.la_window_prefill(q, k, k, 4, k_cache=torch.zeros(1, 1, 5, 64), v_cache=torch.zeros(1, 1, 4, 64))
+    with pytest.raises(ValueError, match="pos"):
+        la.la_window_decode_step(q[:, :, 0], k[:, :, 0], k[:, :, 0], torch.zeros(1, 1, 4, 64), torch.zeros(1, 1, 4, 64),
+                                 torch.zeros(1), 4)
