@@ -627,33 +627,12 @@ ssm_step_kernel(const __grid_constant__ SsmArgs a, int tiles_per_group)
     const int c0 = grp * per + cg0, nch = min(32, per - cg0);
     const int n = a.n;
 
-    float dt = 0.f, u = 0.f, add = 0.f, gate = 1.f;
-    if (lane < nch) {
-        const int c = c0 + lane;
-        const float xv = to_f32<T>(((const T*)a.x)[b * a.st.x_batch + c]);
-        dt = to_f32<T>(((const T*)a.delta)[b * a.st.delta_batch + c]) + (a.delta_bias ? a.delta_bias[c] : 0.f);
-        if (a.softplus) dt = softplus(dt);
-        u = dt * xv;
-        if (a.skip) add = a.skip[c] * xv;
-        if (a.z) gate = silu<T>(to_f32<T>(((const T*)a.z)[b * a.st.z_batch + c]));
-    }
-    const int part = lane % P, sub = lane / P;     // this lane's states of channel (32 / P) * it + sub
-    const int s0 = part * V;
-    float Bv[V], Cv[V];
-    {
-        const T* bp = (const T*)a.Bm + b * a.st.B_batch + (size_t)grp * n;
-        const T* cp = (const T*)a.Cm + b * a.st.C_batch + (size_t)grp * n;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            Bv[i] = s0 + i < n ? to_f32<T>(bp[s0 + i]) : 0.f;
-            Cv[i] = s0 + i < n ? to_f32<T>(cp[s0 + i]) : 0.f;
-        }
-    }
     constexpr int STEP = 32 / P;                   // channels per pass
     constexpr int U = P < 4 ? P : 4;               // passes whose loads are in flight together
-    float y = 0.f;
-    for (int i0 = 0; i0 < P; i0 += U) {
-        float hv[U][V], av[U][V];
+    const int part = lane % P, sub = lane / P;     // this lane's states of channel STEP * pass + sub
+    const int s0 = part * V;
+    float hv[U][V], av[U][V];
+    auto load = [&](int i0) {
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int ch = (i0 + i) * STEP + sub;
@@ -674,6 +653,32 @@ ssm_step_kernel(const __grid_constant__ SsmArgs a, int tiles_per_group)
                 }
             }
         }
+    };
+    load(0);     // the states are on their way while the scalars are prepared
+
+    float dt = 0.f, u = 0.f, add = 0.f, gate = 1.f;
+    float Bv[V], Cv[V];
+    {
+        const T* bp = (const T*)a.Bm + b * a.st.B_batch + (size_t)grp * n;
+        const T* cp = (const T*)a.Cm + b * a.st.C_batch + (size_t)grp * n;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            Bv[i] = s0 + i < n ? to_f32<T>(bp[s0 + i]) : 0.f;
+            Cv[i] = s0 + i < n ? to_f32<T>(cp[s0 + i]) : 0.f;
+        }
+    }
+    if (lane < nch) {
+        const int c = c0 + lane;
+        const float xv = to_f32<T>(((const T*)a.x)[b * a.st.x_batch + c]);
+        dt = to_f32<T>(((const T*)a.delta)[b * a.st.delta_batch + c]) + (a.delta_bias ? a.delta_bias[c] : 0.f);
+        if (a.softplus) dt = softplus(dt);
+        u = dt * xv;
+        if (a.skip) add = a.skip[c] * xv;
+        if (a.z) gate = silu<T>(to_f32<T>(((const T*)a.z)[b * a.st.z_batch + c]));
+    }
+    float y = 0.f;
+    for (int i0 = 0; i0 < P; i0 += U) {
+        if (i0 > 0) load(i0);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int ch = (i0 + i) * STEP + sub;
