@@ -287,11 +287,12 @@ window_decode_mma(const __grid_constant__ WindowArgs a, int chunks)
     for (; s < s1; s += kMmaWarps * 16) {
         const int next = s + kMmaWarps * 16;
         ahead(s + kAhead * kMmaWarps * 16);
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        // two sums of every other step: half the chain of dependent products
+        float c[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int x = 0; x < KS; ++x) {
             mma_16816(c, kr[0][x].x, kr[1][x].x, kr[0][x].y, kr[1][x].y, qr[x].x, qr[x].y);
-            mma_16816(c, kr[0][x].z, kr[1][x].z, kr[0][x].w, kr[1][x].w, qr[x].z, qr[x].w);
+            mma_16816(c1, kr[0][x].z, kr[1][x].z, kr[0][x].w, kr[1][x].w, qr[x].z, qr[x].w);
         }
         if (next < s1) load_k(next);
         // c: keys g (0, 1) and g + 8 (2, 3) of heads 2t, 2t + 1
@@ -299,8 +300,8 @@ window_decode_mma(const __grid_constant__ WindowArgs a, int chunks)
         float top[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            c[j] = on0 ? c[j] * sl : -INFINITY;
-            c[2 + j] = on1 ? c[2 + j] * sl : -INFINITY;
+            c[j] = on0 ? (c[j] + c1[j]) * sl : -INFINITY;
+            c[2 + j] = on1 ? (c[2 + j] + c1[2 + j]) * sl : -INFINITY;
             top[j] = fmaxf(c[j], c[2 + j]);
 #pragma unroll
             for (int w = 4; w < 32; w *= 2) top[j] = fmaxf(top[j], __shfl_xor_sync(~0u, top[j], w));
@@ -435,12 +436,18 @@ template <int D, int DV>
 cudaError_t launch_dd(const WindowArgs& a)
 {
     if (a.dtype == LA_BF16) {
-        // few sequences: eight warps a CTA halve the serial walk of a warp; many: four warps and three CTAs an SM
+        // Few CTAs (one wave of one an SM, or two waves in small clusters, which pack): eight warps
+        // each halve a warp's serial walk (128 units of 4100 slots 58 -> 52 us).  Else four warps, three
+        // CTAs an SM: at least 64 slots a CTA up to four an SM, and eight an SM, which even out the last
+        // wave, while a CTA keeps 512 slots (512 units of 4100 slots 184 -> 173 us; with 257 slots a CTA
+        // its 4 us of set-up and joining cost more than that: 256 units of 1028 slots 33 -> 52 us).
         const int wide = splits_for(a, kMmaHeads, 148, 128, kMaxSplit);
         const int chunks = (a.Hq / a.Hkv + kMmaHeads - 1) / kMmaHeads;
-        if ((long long)a.B * a.Hkv * chunks * wide <= 148)
+        const long long ctas = (long long)a.B * a.Hkv * chunks * wide;
+        if (ctas <= 148 || (wide <= 2 && ctas <= 296))
             return launch_clusters(window_decode_mma<D, DV, 8>, a, kMmaHeads, 256, wide);
-        return launch_clusters(window_decode_mma<D, DV, 4>, a, kMmaHeads, 128, splits_for(a, kMmaHeads, 148 * 4, 64, 8));
+        const int fill = splits_for(a, kMmaHeads, 148 * 4, 64, 8), even = splits_for(a, kMmaHeads, 148 * 8, 512, 8);
+        return launch_clusters(window_decode_mma<D, DV, 4>, a, kMmaHeads, 128, fill > even ? fill : even);
     }
     return launch_clusters(window_decode_simt<float, D, DV>, a, kHeads, kThreads, splits_for(a, kHeads, 148 * 4, 64, 8));
 }
