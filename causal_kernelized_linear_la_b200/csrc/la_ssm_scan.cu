@@ -632,14 +632,17 @@ ssm_step_kernel(const __grid_constant__ SsmArgs a, int tiles_per_group)
     const int part = lane % P, sub = lane / P;     // this lane's states of channel STEP * pass + sub
     const int s0 = part * V;
     float hv[U][V], av[U][V];
+    // this lane's place in the tile's states and decay rates; a pass is STEP channels on
+    const int mine = sub * n + s0;
+    float* const hb = a.h_out + ((size_t)b * a.D + c0) * n + mine;
+    const float* const ab = a.A + (size_t)c0 * n + mine;
+    const int last = s0 < n ? nch - sub : 0;       // passes below last / STEP hold a channel
     auto load = [&](int i0) {
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int ch = (i0 + i) * STEP + sub;
-            const size_t c = (size_t)(c0 + (ch < nch ? ch : 0));
-            const float* hp = a.h_out + ((size_t)b * a.D + c) * n + s0;
-            const float* ap = a.A + c * n + s0;
-            const bool on = ch < nch && s0 < n;
+            const float* hp = hb + (i0 + i) * STEP * n;
+            const float* ap = ab + (i0 + i) * STEP * n;
+            const bool on = (i0 + i) * STEP < last;
             if (V == 4) {
                 const float4 hq = on ? __ldcs(reinterpret_cast<const float4*>(hp)) : make_float4(0.f, 0.f, 0.f, 0.f);
                 const float4 aq = on ? *reinterpret_cast<const float4*>(ap) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -659,12 +662,12 @@ ssm_step_kernel(const __grid_constant__ SsmArgs a, int tiles_per_group)
     float dt = 0.f, u = 0.f, add = 0.f, gate = 1.f;
     float Bv[V], Cv[V];
     {
-        const T* bp = (const T*)a.Bm + b * a.st.B_batch + (size_t)grp * n;
-        const T* cp = (const T*)a.Cm + b * a.st.C_batch + (size_t)grp * n;
+        const T* bp = (const T*)a.Bm + b * a.st.B_batch + (size_t)grp * n + s0;
+        const T* cp = (const T*)a.Cm + b * a.st.C_batch + (size_t)grp * n + s0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            Bv[i] = s0 + i < n ? to_f32<T>(bp[s0 + i]) : 0.f;
-            Cv[i] = s0 + i < n ? to_f32<T>(cp[s0 + i]) : 0.f;
+            Bv[i] = s0 + i < n ? to_f32<T>(bp[i]) : 0.f;
+            Cv[i] = s0 + i < n ? to_f32<T>(cp[i]) : 0.f;
         }
     }
     if (lane < nch) {
@@ -689,8 +692,8 @@ ssm_step_kernel(const __grid_constant__ SsmArgs a, int tiles_per_group)
                 hv[i][j] = fmaf(ex2_approx(d * av[i][j]), hv[i][j], ux * Bv[j]);
                 acc = fmaf(Cv[j], hv[i][j], acc);
             }
-            if (ch < nch && s0 < n) {
-                float* hp = a.h_out + ((size_t)b * a.D + c0 + ch) * n + s0;
+            if ((i0 + i) * STEP < last) {
+                float* hp = hb + (i0 + i) * STEP * n;
                 if (V == 4) {
                     __stcs(reinterpret_cast<float4*>(hp), make_float4(hv[i][0], hv[i][V > 1 ? 1 : 0], hv[i][V > 2 ? 2 : 0],
                                                                       hv[i][V > 3 ? 3 : 0]));
