@@ -542,6 +542,9 @@ def la_ssm_step(x, delta, A, B, C, h, D=None, z=None, delta_bias=None, delta_sof
     return out
 
 
+_INT = 1 << 31
+
+
 def _head_strides(t, rows, name):
     """(batch, head, row) strides of [B, H, N, .] (rows) or [B, H, .]; an axis of one entry has none that matters."""
     shape, stride = t.shape, t.stride()
@@ -557,6 +560,8 @@ def _window_checks(q, k, v, out, k_cache, v_cache, pos, window, sinks, scale):
     rows = len(qs) == 4
     B, Hq, d, Hkv, dv = qs[0], qs[1], qs[-1], ks[1], vs[-1]
     N = qs[2] if rows else 1
+    if not (-_INT < window < _INT and -_INT < sinks < _INT):
+        raise ValueError(f"window and sinks must fit 32 bits, got {window} and {sinks}")
     if ks[0] != B or vs[0] != B or vs[1] != Hkv or ks[-1] != d or (rows and not ks[2] == vs[2] == N):
         raise ValueError(f"q, k, v do not fit: {list(qs)}, {list(ks)}, {list(vs)}")
     if out.shape != ((B, Hq, N, dv) if rows else (B, Hq, dv)):

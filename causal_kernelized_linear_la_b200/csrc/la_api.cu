@@ -178,6 +178,9 @@ size_t extent(int B, int N, long long cols, long long batch, long long row, size
     return ((size_t)(B - 1) * batch + (size_t)(N - 1) * row + cols) * e;
 }
 
+// Tokens of a state-space call's sequences: token numbers add up inside 32 bits.
+constexpr int kMostRows = 1 << 30;
+
 // Sequences of one launch: all of them, or kMaxSeqLens where lengths travel with the launch.
 int launch_group(const int* lens) { return lens ? kMaxSeqLens : 32768; }
 
@@ -579,7 +582,7 @@ la_status la_ssm_conv(const void* x, const float* weight, const float* bias, con
     if (!cfg) return LA_ERR_INVALID;
     if (B < 0 || N < 0 || D < 0 || w < 1 || x_batch < 0 || x_row < 0) return LA_ERR_INVALID;
     if (cfg->dtype != LA_F32 && cfg->dtype != LA_BF16) return LA_ERR_INVALID;
-    if (w > 8) return LA_ERR_UNSUPPORTED;
+    if (w > 8 || N > la::kMostRows) return LA_ERR_UNSUPPORTED;
     if (!la::lens_ok(seq_lens, B, N)) return LA_ERR_INVALID;
     if (B == 0 || D == 0) return LA_OK;
     if (N > 0 && (!x || !weight || !out)) return LA_ERR_INVALID;
@@ -633,6 +636,7 @@ la_status la_ssm_scan(const void* x, const void* delta, const float* A, const vo
     const la_status st =
         la::check_ssm(x, delta, A, Bm, Cm, D_skip, z, delta_bias, out, h_out, N, B, D, G, n, strides, cfg);
     if (st != LA_OK) return st;
+    if (N > la::kMostRows) return LA_ERR_UNSUPPORTED;
     if (!la::lens_ok(seq_lens, B, N)) return LA_ERR_INVALID;
     const size_t states = (size_t)B * D * n * sizeof(float);
     if (la::overlap(h_out, states, cfg->S0, states)) return LA_ERR_INVALID;

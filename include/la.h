@@ -16,6 +16,10 @@
  *     o_t = S_t^T q_t            (no feature map, no normaliser)
  *   ("Efficient attention variants" §7.4; "What Is Linear Attention?" §5.2-5.3)
  *
+ * and, further down, two other token mixers whose memory does not grow with the
+ * sequence: a selective state-space layer (la_ssm_*) and softmax attention over
+ * a sliding window with sinks (la_window_*); their own conventions stand there.
+ *
  * Prefill runs chunkwise: parallel inside a chunk, state carried between
  * chunks ("Efficient attention variants" §8).  Decode applies the recurrence
  * to one token per (sequence, head) against a resident state.
@@ -317,7 +321,8 @@ LA_API la_status la_causal_conv(const void* x, const float* weight, const void* 
  * - seq_lens is a HOST array of B lengths of a right-padded batch, each
  *   0 <= seq_lens[b] <= N, or NULL (every sequence holds N tokens).  Padding rows
  *   never reach a result, whatever they hold; padding rows of out are not written.
- * - B, N, G >= 0 and D >= 0 of any size with D a multiple of G; 1 <= n <= 64.
+ * - B, G >= 0, 0 <= N <= 2^30 and D >= 0 of any size with D a multiple of G;
+ *   1 <= n <= 64.
  */
 
 /* Strides in elements (>= 0) of the rows of a state-space call; NULL in place
@@ -382,7 +387,9 @@ LA_API la_status la_ssm_scan(const void* x, const void* delta, const float* A, c
                              const int* seq_lens, int B, int N, int D, int G, int n, int delta_softplus,
                              const la_ssm_strides* strides, const la_config* cfg);
 
-/* Device scratch of la_ssm_scan for these sizes; 0 when the tokens run in one segment. */
+/* Device scratch of la_ssm_scan for these sizes: the summaries of the segments
+ * that a long prompt of few channels is cut into; 0 when it runs in one.  Dead
+ * after the call's work completes; two calls in flight need two. */
 LA_API size_t la_ssm_scan_workspace_bytes(int B, int N, int D, int G, int n);
 
 /*
@@ -448,8 +455,9 @@ typedef struct {
  * see enters its sum with weight zero.  k may hold anything there.
  * bf16 runs on the tensor cores and rounds the weights w_ij (relative to the
  * row's running reference) to bf16; fp32 keeps fp32 arithmetic throughout.
+ * One kernel, and with a cache a second one that moves the tokens into it.
  * LA_ERR_INVALID, LA_ERR_UNSUPPORTED, LA_ERR_ALIGN as elsewhere; LA_ERR_INVALID
- * too if out, or a cache, overlaps k or v.
+ * too if a cache, or a dense out, overlaps k or v.
  */
 LA_API la_status la_window_prefill(const void* q, const void* k, const void* v, void* out,
                                    void* k_cache, void* v_cache, const int* pos, const int* seq_lens,
@@ -477,7 +485,10 @@ LA_API la_status la_window_decode_step(const void* q, const void* k, const void*
  * (i < n; a call launches 1 to 16 kernels, la_prefill_kernel_count gives the
  * number for a prefill: bf16 LA_PLAIN/LA_DECAY prefill = segment summaries,
  * scan, chunk loop; bf16 LA_GATED_DELTA prefill = chunk prep and chain per
- * part; every other path, la_causal_conv included, one kernel).  events are cudaEvent_t handles
+ * part; la_ssm_scan = segment summaries, if it needs a workspace, and the scan;
+ * la_window_prefill = attention and, with a cache, the cache's update; every
+ * other path, la_causal_conv included, one kernel; a batch with lengths of more
+ * than 128 sequences runs as several such launches).  events are cudaEvent_t handles
  * owned by the caller, who must keep them alive while the hook is set; n = 0
  * turns it off.  The setting is process-wide and not thread-safe: set it
  * only while no other thread launches through this library.  Returns

@@ -30,6 +30,7 @@ def test_conv_refusals():
     assert _conv(w=0) == la.LA_ERR_INVALID
     assert _conv(w=9) == la.LA_ERR_UNSUPPORTED
     assert _conv(xt=-1) == la.LA_ERR_INVALID
+    assert _conv(N=(1 << 30) + 1) == la.LA_ERR_UNSUPPORTED
     assert _conv(x=0) == la.LA_ERR_INVALID
     assert _conv(out=0) == la.LA_ERR_INVALID
     assert _conv(cfg=_cfg(dtype=5)) == la.LA_ERR_INVALID
@@ -58,6 +59,7 @@ def test_scan_refusals():
     assert _scan(N=-1) == la.LA_ERR_INVALID
     assert _scan(n=0) == la.LA_ERR_INVALID
     assert _scan(n=65) == la.LA_ERR_UNSUPPORTED
+    assert _scan(N=(1 << 30) + 1) == la.LA_ERR_UNSUPPORTED
     assert _scan(G=3) == la.LA_ERR_INVALID                         # 16 channels in 3 groups
     assert _scan(G=0) == la.LA_ERR_INVALID
     assert _scan(x=0) == la.LA_ERR_INVALID
@@ -186,6 +188,8 @@ def test_binding_checks():
     q, k = torch.zeros(1, 2, 8, 64), torch.zeros(1, 1, 8, 64)
     with pytest.raises(ValueError, match="CUDA"):
         la.la_window_prefill(q, k, k, 4)
+    with pytest.raises(ValueError, match="32 bits"):
+        la.la_window_prefill(q, k, k, (1 << 32) + 4)      # would wrap to 4
     with pytest.raises(ValueError, match="do not fit"):
         la.la_window_prefill(q, k, k[:, :, :7], 4)
     with pytest.raises(ValueError, match="k_cache"):
