@@ -16,7 +16,11 @@
 // once a value, off the recurrence's path.
 // The decay needs one exponential per (token, channel, state): the SFU's 16 a
 // clock and SM bound the scan (at n = 16 its 2^x alone take three times as
-// long as reading delta, x, z and writing y), not memory.
+// long as reading delta, x, z and writing y), not memory.  At 8192 tokens x 4096
+// channels x 16 states (bf16, softplus, skip, gate) those two floors are 119 and
+// 41 us; the kernel takes 259.  The recurrence warps issue in order and need about
+// 48 clocks a token where the SFU alone needs 32: without exponentials 244 us, with
+// idle helpers 199 to 217 (both measured on copies).
 //
 // Few channels leave SMs idle, so a long sequence is cut into segments: a
 // first kernel runs every segment but the last from a zero state and keeps
@@ -38,6 +42,15 @@ constexpr int kFin = 128;      // threads that finish y
 constexpr int kBufs = 3;       // prepared tiles: one in the recurrence, one being finished, one being prepared
 constexpr int kRaw = kBufs + 4;   // tiles of raw rows: those of the prepared tiles and one being prepared, the others in flight
 constexpr float kLog2e = 1.4426950408889634f;
+// The SFU's 2^x comes out low on average (measured, in units of 2^-24: 0.09 to
+// 0.17 for x in [-0.003, 0], 0.30 to 0.44 for x in [-1, -0.003]), and a slow state's
+// many decays add that up.  So each exponent is lifted by the middle of its
+// range, in log2 units; which one goes by the step size against a limit per
+// lane, where the exponent in the lane's middle passes 0.003.  2^lift itself is
+// exactly 1: a step of zero changes nothing.
+constexpr float kLiftSlow = 0.12f * 5.9604645e-8f * kLog2e, kLiftFast = 0.36f * 5.9604645e-8f * kLog2e;
+constexpr float kSlow = 0.003f;
+__device__ __forceinline__ float lift_limit(float a2_first, float a2_last) { return kSlow / (0.5f * fabsf(a2_first + a2_last)); }
 
 struct Lens {
     int use;
@@ -233,6 +246,7 @@ ssm_scan_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ Lens 
         // exponentials (8 clocks each) and the chain overlap in one warp; the
         // loads also come before the stores of y, above which none is moved.
         constexpr int NB = NS <= 2 ? 4 : NS == 4 ? 4 : 2, NH = (NS + 1) / 2;
+        const float slow_below = lift_limit(unpack2(A2[0]).x, NS > 1 ? unpack2(A2[NH - 1]).y : unpack2(A2[0]).x);
         float2 dv[2][NB];                               // (dt, dt x)
         f2 dec[2][NB][NH], bv[2][NB][NH], cv[2][NB][NH];
         auto load = [&](int k, int t0, int w) {
@@ -266,9 +280,14 @@ ssm_scan_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ Lens 
         };
         auto decays = [&](int t, int w) {
             const f2 dt = pack2(dv[w][t].x, dv[w][t].x);
+            // the first of each two tokens decides: 259 us, where every token deciding takes
+            // 266; one lift for all exponents takes 255, but left some states' errors at two to
+            // four times those of exact decays
+            const float up = dv[w][t & ~1].x < slow_below ? kLiftSlow : kLiftFast;
+            const f2 lift = pack2(up, up);
 #pragma unroll
             for (int i = 0; i < NH; ++i) {
-                const float2 e = unpack2(mul2(dt, A2[i]));
+                const float2 e = unpack2(fma2(dt, A2[i], lift));
                 dec[w][t][i] = pack2(ex2_approx(e.x), NS > 1 ? ex2_approx(e.y) : 0.f);
             }
         };
@@ -686,10 +705,12 @@ ssm_step_kernel(const __grid_constant__ SsmArgs a, int tiles_per_group)
         for (int i = 0; i < U; ++i) {
             const int ch = (i0 + i) * STEP + sub;
             const float d = __shfl_sync(~0u, dt, ch) * kLog2e, ux = __shfl_sync(~0u, u, ch);
+            // the lift of the prompt scan's decays
+            const float up = fabsf(d * (av[i][0] + av[i][V - 1])) < 2.f * kSlow ? kLiftSlow : kLiftFast;
             float acc = 0.f;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                hv[i][j] = fmaf(ex2_approx(d * av[i][j]), hv[i][j], ux * Bv[j]);
+                hv[i][j] = fmaf(ex2_approx(fmaf(d, av[i][j], up)), hv[i][j], ux * Bv[j]);
                 acc = fmaf(Cv[j], hv[i][j], acc);
             }
             if ((i0 + i) * STEP < last) {

@@ -232,6 +232,36 @@ def test_large_and_extreme_values():
     assert torch.allclose(y.double(), want, rtol=10 * 2.0 ** -24, atol=0)
     y, h = la.la_ssm_scan(x, torch.zeros_like(x), A, bc, bc)  # nothing is written
     assert (y == 0).all() and (h == 0).all()
+    h0 = torch.randn(1, 8, 4, device="cuda")
+    _, h = la.la_ssm_scan(x, torch.zeros_like(x), A, bc, bc, h0=h0)      # and nothing forgotten: every decay is 1
+    assert torch.equal(h, h0)
+    la.la_ssm_step(x[:, 0], torch.zeros_like(x[:, 0]), A, bc[:, 0], bc[:, 0], h)
+    assert torch.equal(h, h0)
+
+
+@pytest.mark.parametrize("segments", [False, True])
+def test_slow_states_keep_their_precision(segments):
+    """Decays near 1 over thousands of tokens: a bias of the exponential adds
+    up token by token.  With u = 2^-24: a decay's mean error is at most 0.06 u
+    for these exponents (between -0.0022 and 0 in log2 units), so N tokens shift
+    the state by at most 0.06 N u; the scatter of decay, product and sum is at
+    most 2 u a token and independent, so about 2 u sqrt(N) together.  At N =
+    4096 that is (246 + 128) u of the state's norm; 8 u sqrt(N) = 512 u are allowed."""
+    g = torch.Generator().manual_seed(1)
+    ch, n, N = (32 if segments else 4096), 8, 4096
+    assert (la.la_ssm_scan_workspace_bytes(1, N, ch, 1, n) > 0) == segments
+    x = torch.randn(1, N, ch, generator=g).cuda()
+    dt = (0.0005 + 0.001 * torch.rand(1, N, ch, generator=g)).cuda()
+    bc = torch.randn(1, N, n, generator=g).cuda()
+    A = -(0.2 + 0.8 * torch.rand(ch, n, generator=g)).cuda()
+    h0 = torch.randn(1, ch, n, generator=g).cuda() * 10
+    _, h = la.la_ssm_scan(x, dt, A, bc, bc, h0=h0)
+    ref = h0.double()[0]
+    for t in range(N):
+        k = dt[0, t].double()[:, None]
+        ref = torch.exp(k * A.double()) * ref + k * x[0, t].double()[:, None] * bc[0, t].double()
+    err = ((h[0].double() - ref).norm() / ref.norm()).item()
+    assert err <= 4 * 2 * 2.0 ** -24 * N ** 0.5, err
 
 
 def test_one_event_a_kernel():
