@@ -501,6 +501,8 @@ def la_ssm_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, delta_softpl
     _dense(h_out, (b, ch, n), torch.float32, "h_out")
     if h0 is not None:
         _dense(h0, (b, ch, n), torch.float32, "h0")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     cfg = LaConfig(_dtype_code(x), 0, 0.0, None, _addr(h0), None, None, 0)
     cfg.stream, guard = _on_device(x, (delta, A, B, C, D, z, delta_bias, h0, out, h_out, workspace), stream)
     need = la_ssm_scan_workspace_bytes(b, N, ch, G, n)

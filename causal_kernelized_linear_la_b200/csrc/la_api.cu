@@ -292,6 +292,8 @@ la_status check_window(WindowArgs* w, const void* q, const void* k, const void* 
     if (!aligned_to(pos, sizeof(int))) return LA_ERR_ALIGN;
     // rows of one head do not share memory
     if (N > 1 && (s.q_row < d || s.k_row < d || s.v_row < dv || s.out_row < dv)) return LA_ERR_INVALID;
+    // nor do two heads or sequences of out
+    if (work > 0 && ((Hq > 1 && s.out_head == 0) || (B > 1 && s.out_batch == 0))) return LA_ERR_INVALID;
     if (work > 0) {
         const size_t cap = (size_t)window + sinks;
         const size_t ks = extent4(B, Hkv, N, d, s.k_batch, s.k_head, s.k_row, e);

@@ -423,9 +423,11 @@ LA_API la_status la_ssm_step(const void* x, const void* delta, const float* A, c
  *
  * Query head h reads kv head h / (Hq / Hkv); Hq is a multiple of Hkv.  d, dv in
  * {64, 128}; window >= 1, sinks >= 0; N <= 65535 * 256 and, with a cache,
- * sinks + window < 2^30 (LA_ERR_UNSUPPORTED); positions stay below 2^31; rows of one
- * head are at least d (dv) elements apart.  Sums, maxima and outputs accumulate in fp32.  All pointers are
- * 16-byte aligned, and so are the rows (strides are multiples of 16 bytes).
+ * sinks + window < 2^30 (LA_ERR_UNSUPPORTED); positions stay below 2^31; rows of
+ * one head are at least d (dv) elements apart; several query heads or sequences
+ * may read one head of q, k or v (stride 0), but each has its own rows of out.
+ * Sums, maxima and outputs accumulate in fp32.  All pointers are 16-byte
+ * aligned, and so are the rows (strides are multiples of 16 bytes).
  */
 
 /* Strides in elements (>= 0); NULL in place of this struct means dense

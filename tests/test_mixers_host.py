@@ -197,3 +197,14 @@ def test_binding_checks():
     with pytest.raises(ValueError, match="pos"):
         la.la_window_decode_step(q[:, :, 0], k[:, :, 0], k[:, :, 0], torch.zeros(1, 1, 4, 64), torch.zeros(1, 1, 4, 64),
                                  torch.zeros(1), 4)
+
+
+def test_outputs_that_share_memory_are_refused():
+    dense = [1024, 512, 64] * 4
+    assert _window(Hq=2, Hkv=1, st=LaWindowStrides(*dense[:10], 0, 64)) == la.LA_ERR_INVALID     # heads of out
+    assert _window(B=2, st=LaWindowStrides(*dense[:9], 0, 512, 64)) == la.LA_ERR_INVALID         # sequences of out
+    x, A, bc = torch.zeros(1, 4096, 32), torch.zeros(32, 16), torch.zeros(1, 4096, 16)
+    need = la.la_ssm_scan_workspace_bytes(1, 4096, 32, 1, 16)
+    assert need > 0
+    with pytest.raises(ValueError, match="workspace"):        # many bytes by its shape, one in memory
+        la.la_ssm_scan(x, x, A, bc, bc, workspace=torch.zeros(1, dtype=torch.uint8).expand(need))
