@@ -77,9 +77,9 @@ __device__ __forceinline__ void row_store(T* p, const float (&f)[V])
     *reinterpret_cast<Row<T, V>*>(p) = r;
 }
 
-// fp32 outputs take the accurate exponential; bf16 rounding hides the fast one's error
+// bf16 rounding hides the shorter form's error
 template <typename T> __device__ __forceinline__ float silu(float y);
-template <> __device__ __forceinline__ float silu<float>(float y) { return y / (1.f + expf(-y)); }
+template <> __device__ __forceinline__ float silu<float>(float y) { return silu_f32(y); }
 template <> __device__ __forceinline__ float silu<__nv_bfloat16>(float y) { return silu_approx(y); }
 
 // V channels' filters [V][W] and biases

@@ -73,7 +73,7 @@ __device__ __forceinline__ float softplus(float v)
     return fmaf(2.f * r, p, fmaxf(v, 0.f));
 }
 template <typename T> __device__ __forceinline__ float silu(float v);
-template <> __device__ __forceinline__ float silu<float>(float v) { return v / (1.f + expf(-v)); }
+template <> __device__ __forceinline__ float silu<float>(float v) { return silu_f32(v); }
 template <> __device__ __forceinline__ float silu<__nv_bfloat16>(float v) { return silu_approx(v); }
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, uint32_t src_bytes)

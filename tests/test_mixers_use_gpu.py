@@ -282,3 +282,18 @@ def test_one_event_a_kernel():
         torch.cuda.synchronize()
         # events of kernels that ran lie behind the start, the others before it
         assert [start.elapsed_time(e) >= 0 for e in events] == [i < kernels for i in range(3)], name
+
+
+def test_silu_in_fp32():
+    """One tap of weight one: out = silu(x).  Steps of u = 2^-24: the SFU's 2^x 4
+    (two places), its first-order correction and product 2, 1 + h 1, the
+    reciprocal after its Newton step 1, two products 2: 10 u together."""
+    x = torch.cat([torch.linspace(-80, 80, 200001), torch.logspace(-30, 0, 5000), -torch.logspace(-30, 0, 5000)])
+    x = x[:x.numel() // 8 * 8].view(1, -1, 8).cuda()
+    y, _ = la.la_ssm_conv(x, torch.ones(8, 1, device="cuda"))
+    want = torch.nn.functional.silu(x.double())
+    assert ((y.double() - want).abs() <= 10 * 2.0 ** -24 * want.abs()).all()
+    far = torch.tensor([float("inf"), 1e30, -1e4, -120.0, 0.0, -0.0, float("nan"), 100.0], device="cuda").view(1, 1, 8)
+    y, _ = la.la_ssm_conv(far, torch.ones(8, 1, device="cuda"))
+    y = y.flatten().tolist()
+    assert y[0] == float("inf") and y[1] == far[0, 0, 1].item() and y[2:6] == [0, 0, 0, 0] and y[6] != y[6] and y[7] == 100
