@@ -18,7 +18,7 @@
 // clock and SM bound the scan (at n = 16 its 2^x alone take three times as
 // long as reading delta, x, z and writing y), not memory.  At 8192 tokens x 4096
 // channels x 16 states (bf16, softplus, skip, gate) those two floors are 119 and
-// 41 us; the kernel takes 259.  The recurrence warps issue in order and need about
+// 41 us; the kernel takes 264.  The recurrence warps issue in order and need about
 // 48 clocks a token where the SFU alone needs 32: without exponentials 244 us, with
 // idle helpers 199 to 217 (both measured on copies).
 //
@@ -92,45 +92,51 @@ __device__ __forceinline__ void bar_arrive(uint32_t id, uint32_t count)
 }
 
 // A tile of `rows` (of ROWS) x `cols` (of PITCH) elements of a row-major
-// tensor into shared memory, zeros elsewhere, in pieces of BYTES (4, or the
-// element itself), by the preparing threads: rows that do not start on 16 bytes.
-template <typename T, int ROWS, int PITCH, int BYTES>
-__device__ __forceinline__ void load_pieces(T* dst, const T* src, long long row_stride, int rows, int cols, int tid)
+// tensor into shared memory, zeros elsewhere, by the preparing threads, where
+// rows do not start on 16 bytes.  A thread keeps its column: copies of 4 bytes, or ...
+template <typename T, int ROWS, int PITCH>
+__device__ __forceinline__ void copy_words(T* dst, const T* src, long long row_stride, int rows, int cols, int tid)
 {
-    constexpr int PER = BYTES / (int)sizeof(T), N = PITCH / PER, STEP = kPrep / N;   // pieces of a row, rows of a pass
+    constexpr int PER = 4 / (int)sizeof(T), N = PITCH / PER, STEP = kPrep / N;   // pieces of a row, rows of a pass
     static_assert(kPrep % N == 0 && ROWS % STEP == 0, "a thread keeps its columns");
     const int c = tid % N * PER, t0 = tid / N;
     const int left = min(PER, max(0, cols - c));
     const T* s = src + (left > 0 ? t0 * row_stride + c : 0);
     const long long step = left > 0 ? STEP * row_stride : 0;
     T* d = dst + t0 * PITCH + c;
-    if (BYTES == 4) {
-        if (rows >= ROWS) {
+    if (rows >= ROWS) {
 #pragma unroll
-            for (int i = 0; i < ROWS / STEP; ++i, s += step) cp_async4(d + i * STEP * PITCH, s, left * sizeof(T));
-        } else {
-#pragma unroll
-            for (int i = 0; i < ROWS / STEP; ++i, s += step) {
-                const bool on = t0 + i * STEP < rows;
-                cp_async4(d + i * STEP * PITCH, on ? s : src, on ? left * sizeof(T) : 0);
-            }
-        }
+        for (int i = 0; i < ROWS / STEP; ++i, s += step) cp_async4(d + i * STEP * PITCH, s, left * sizeof(T));
     } else {
-        // the element itself through registers, eight loads at a time
 #pragma unroll
-        for (int i0 = 0; i0 < ROWS / STEP; i0 += 8) {
-            T v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i, s += step)
-                v[i] = i0 + i < ROWS / STEP && left > 0 && t0 + (i0 + i) * STEP < rows ? *s : from_f32<T>(0.f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i0 + i < ROWS / STEP) d[(i0 + i) * STEP * PITCH] = v[i];
+        for (int i = 0; i < ROWS / STEP; ++i, s += step) {
+            const bool on = t0 + i * STEP < rows;
+            cp_async4(d + i * STEP * PITCH, on ? s : src, on ? left * sizeof(T) : 0);
         }
     }
 }
-
-template <int N> struct Int { static constexpr int value = N; };
+// ... single elements (2 bytes are no size of a copy) through registers: loaded
+// for one tile while the tile before it is put down.
+template <typename T, int ROWS, int PITCH>
+struct Elements {
+    static constexpr int STEP = kPrep / PITCH, COUNT = ROWS / STEP;
+    static_assert(kPrep % PITCH == 0 && ROWS % STEP == 0, "a thread keeps its column");
+    T v[COUNT];
+    __device__ __forceinline__ void load(const T* src, long long row_stride, int rows, int cols, int tid)
+    {
+        const int c = tid % PITCH, t0 = tid / PITCH;
+        const T* s = src + t0 * row_stride + c;
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i, s += STEP * row_stride)
+            v[i] = c < cols && t0 + i * STEP < rows ? *s : from_f32<T>(0.f);
+    }
+    __device__ __forceinline__ void store(T* dst, int tid) const
+    {
+        T* d = dst + tid / PITCH * PITCH + tid % PITCH;
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) d[i * STEP * PITCH] = v[i];
+    }
+};
 
 // Two neighbouring values (the first at an even place).
 template <typename T> __device__ __forceinline__ float2 load2(const T* p);
@@ -186,10 +192,13 @@ enum Bars : uint32_t { kReady = 1, kDone = kReady + kBufs, kPrepBar = kDone + kB
 
 // grid: (channel tiles, segments, sequences).  SUMMARY: the first kernel of a
 // segmented scan; otherwise outputs and the final state.
-template <typename T, int NS, int LANES, bool SUMMARY>
+// PIECE: how rows come into shared memory, by what their starts are aligned to:
+// copies of 16 bytes, of 4, or single elements of 2 through registers (4096
+// tokens and about 4096 channels x 16 states: bf16 134 us with pieces of 16, 177 of 2;
+// fp32 137 of 16, 191 of 4).
+template <typename T, int NS, int LANES, bool SUMMARY, int PIECE>
 __global__ void __launch_bounds__(Plan<T, NS, LANES>::THREADS, 1)
-ssm_scan_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ Lens lens, int tiles_per_group, int px,
-                int pb)
+ssm_scan_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ Lens lens, int tiles_per_group)
 {
     using P = Plan<T, NS, LANES>;
     constexpr int NP = P::NP, CH = P::CH, TT = P::TT, kRec = P::REC, kThreads = P::THREADS;
@@ -280,8 +289,8 @@ ssm_scan_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ Lens 
         };
         auto decays = [&](int t, int w) {
             const f2 dt = pack2(dv[w][t].x, dv[w][t].x);
-            // the first of each two tokens decides: 259 us, where every token deciding takes
-            // 266; one lift for all exponents takes 255, but left some states' errors at two to
+            // the first of each two tokens decides: 4 us of 260 more than one lift for all
+            // exponents (every token deciding: 11 us), but that left some states' errors at two to
             // four times those of exact decays
             const float up = dv[w][t & ~1].x < slow_below ? kLiftSlow : kLiftFast;
             const f2 lift = pack2(up, up);
@@ -353,12 +362,11 @@ ssm_scan_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ Lens 
         for (int j = 0; j < 2; ++j) bias[j] = a.delta_bias && cc + j < nch ? a.delta_bias[c0 + cc + j] : 0.f;
 
         // this thread's 16-byte pieces of every tile, where all rows start on 16 bytes
-        const bool wide = px == 16 && pb == 16;
         const char* src[P::SLOTS];
         long long step[P::SLOTS];
         int dst[P::SLOTS], rowof[P::SLOTS];      // rowof: the piece's token of the tile, past TT where there is nothing to read
         uint32_t bytes[P::SLOTS];
-        if (wide) {
+        if constexpr (PIECE == 16) {
 #pragma unroll
             for (int i = 0; i < P::SLOTS; ++i) {
                 const int e = tid + i * kPrep;
@@ -379,12 +387,16 @@ ssm_scan_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ Lens 
                 if (e >= P::PIECES) dst[i] = -1;
             }
         }
+        Elements<T, TT, CH> ex, ed, ez;
+        Elements<T, TT, P::BCP> eb, ec;
+        static_assert(kRaw - kBufs - 1 >= 2, "single elements reach shared memory one tile later than copies");
         auto raw = [&](int k) { return sm + (k % kRaw) * P::STAGE; };
         auto fetch = [&](int k) {
-            if (k < nt) {
-                unsigned char* st = raw(k);
-                const int rows = s1 - s0 - k * TT;
-                if (wide) {
+            const int rows = s1 - s0 - k * TT;
+            [[maybe_unused]] const long long t = (long long)k * TT;
+            if constexpr (PIECE == 16) {
+                if (k < nt) {
+                    unsigned char* st = raw(k);
 #pragma unroll
                     for (int i = 0; i < P::SLOTS; ++i) {
                         if (dst[i] >= 0) {
@@ -393,21 +405,34 @@ ssm_scan_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ Lens 
                         }
                         src[i] += step[i];
                     }
-                } else {
-                    const long long t = (long long)k * TT;
-                    auto narrow = [&](auto piece) {
-                        constexpr int BYTES = decltype(piece)::value;
-                        load_pieces<T, TT, CH, BYTES>((T*)st, xp + t * a.st.x_row, a.st.x_row, rows, nch, tid);
-                        load_pieces<T, TT, CH, BYTES>((T*)(st + P::ROW), dp + t * a.st.delta_row, a.st.delta_row, rows, nch, tid);
-                        if (!SUMMARY && zp)
-                            load_pieces<T, TT, CH, BYTES>((T*)(st + 2 * P::ROW), zp + t * a.st.z_row, a.st.z_row, rows, nch, tid);
-                        load_pieces<T, TT, P::BCP, BYTES>((T*)(st + 3 * P::ROW), bp + t * a.st.B_row, a.st.B_row, rows, a.n, tid);
-                        if (!SUMMARY)
-                            load_pieces<T, TT, P::BCP, BYTES>((T*)(st + 3 * P::ROW + P::BC), cp + t * a.st.C_row, a.st.C_row,
-                                                              rows, a.n, tid);
-                    };
-                    if (px >= 4 && pb >= 4) narrow(Int<4>{});
-                    else narrow(Int<(int)sizeof(T)>{});
+                }
+            } else if constexpr (PIECE == 4) {
+                if (k < nt) {
+                    unsigned char* st = raw(k);
+                    copy_words<T, TT, CH>((T*)st, xp + t * a.st.x_row, a.st.x_row, rows, nch, tid);
+                    copy_words<T, TT, CH>((T*)(st + P::ROW), dp + t * a.st.delta_row, a.st.delta_row, rows, nch, tid);
+                    if (!SUMMARY && zp)
+                        copy_words<T, TT, CH>((T*)(st + 2 * P::ROW), zp + t * a.st.z_row, a.st.z_row, rows, nch, tid);
+                    copy_words<T, TT, P::BCP>((T*)(st + 3 * P::ROW), bp + t * a.st.B_row, a.st.B_row, rows, a.n, tid);
+                    if (!SUMMARY)
+                        copy_words<T, TT, P::BCP>((T*)(st + 3 * P::ROW + P::BC), cp + t * a.st.C_row, a.st.C_row, rows,
+                                                  a.n, tid);
+                }
+            } else {
+                if (k > 0 && k <= nt) {
+                    unsigned char* st = raw(k - 1);
+                    ex.store((T*)st, tid);
+                    ed.store((T*)(st + P::ROW), tid);
+                    if (!SUMMARY && zp) ez.store((T*)(st + 2 * P::ROW), tid);
+                    eb.store((T*)(st + 3 * P::ROW), tid);
+                    if (!SUMMARY) ec.store((T*)(st + 3 * P::ROW + P::BC), tid);
+                }
+                if (k < nt) {
+                    ex.load(xp + t * a.st.x_row, a.st.x_row, rows, nch, tid);
+                    ed.load(dp + t * a.st.delta_row, a.st.delta_row, rows, nch, tid);
+                    if (!SUMMARY && zp) ez.load(zp + t * a.st.z_row, a.st.z_row, rows, nch, tid);
+                    eb.load(bp + t * a.st.B_row, a.st.B_row, rows, a.n, tid);
+                    if (!SUMMARY) ec.load(cp + t * a.st.C_row, a.st.C_row, rows, a.n, tid);
                 }
             }
             cp_async_commit();
@@ -537,33 +562,23 @@ int piece_of(const void* p, long long batch, long long row, int e)
     return m % 16 == 0 ? 16 : m % 4 == 0 ? 4 : e;
 }
 
-template <typename T, int NS, int LANES>
-cudaError_t launch_scan_ns(const SsmArgs& a)
+template <typename T, int NS, int LANES, int PIECE>
+cudaError_t launch_scan_piece(const SsmArgs& a)
 {
     using P = Plan<T, NS, LANES>;
-    const int e = sizeof(T);
     const int per = a.D / a.G, tpg = (per + P::CH - 1) / P::CH;
     Lens lens{};
     lens.use = a.seq_lens != nullptr;
     if (a.seq_lens)
         for (int b = 0; b < a.B; ++b) lens.n[b] = a.seq_lens[b];
-    // a group's channels start per * group elements into a row
-    const long long goff = a.G > 1 ? per : 0, noff = a.G > 1 ? a.n : 0;
-    int px = piece_of(a.x, a.st.x_batch, a.st.x_row, e);
-    px = min(px, piece_of(a.delta, a.st.delta_batch, a.st.delta_row, e));
-    if (a.z) px = min(px, piece_of(a.z, a.st.z_batch, a.st.z_row, e));
-    px = min(px, piece_of(nullptr, goff, 0, e));
-    int pb = piece_of(a.Bm, a.st.B_batch, a.st.B_row, e);
-    pb = min(pb, piece_of(a.Cm, a.st.C_batch, a.st.C_row, e));
-    pb = min(pb, piece_of(nullptr, noff, 0, e));
-    auto main_k = ssm_scan_kernel<T, NS, LANES, false>;
-    auto sum_k = ssm_scan_kernel<T, NS, LANES, true>;
+    auto main_k = ssm_scan_kernel<T, NS, LANES, false, PIECE>;
+    auto sum_k = ssm_scan_kernel<T, NS, LANES, true, PIECE>;
     cudaError_t err = cudaFuncSetAttribute(main_k, cudaFuncAttributeMaxDynamicSharedMemorySize, P::BYTES);
     if (err == cudaSuccess) err = cudaFuncSetAttribute(sum_k, cudaFuncAttributeMaxDynamicSharedMemorySize, P::BYTES);
     if (err != cudaSuccess) return err;
     int stage = 0;
     if (a.segs > 1) {
-        sum_k<<<dim3(tpg * a.G, a.segs - 1, a.B), P::THREADS, P::BYTES, a.stream>>>(a, lens, tpg, px, pb);
+        sum_k<<<dim3(tpg * a.G, a.segs - 1, a.B), P::THREADS, P::BYTES, a.stream>>>(a, lens, tpg);
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
         stage_mark(stage++, a.stream);
     }
@@ -577,9 +592,29 @@ cudaError_t launch_scan_ns(const SsmArgs& a)
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = a.segs > 1 ? 1 : 0;
-    err = cudaLaunchKernelEx(&cfg, main_k, a, lens, tpg, px, pb);
+    err = cudaLaunchKernelEx(&cfg, main_k, a, lens, tpg);
     if (err == cudaSuccess) stage_mark(stage, a.stream);
     return err;
+}
+
+template <typename T, int NS, int LANES>
+cudaError_t launch_scan_ns(const SsmArgs& a)
+{
+    const int e = sizeof(T), per = a.D / a.G;
+    // a group's channels start per * group elements into a row
+    const long long goff = a.G > 1 ? per : 0, noff = a.G > 1 ? a.n : 0;
+    int px = piece_of(a.x, a.st.x_batch, a.st.x_row, e);
+    px = min(px, piece_of(a.delta, a.st.delta_batch, a.st.delta_row, e));
+    if (a.z) px = min(px, piece_of(a.z, a.st.z_batch, a.st.z_row, e));
+    px = min(px, piece_of(nullptr, goff, 0, e));
+    int pb = piece_of(a.Bm, a.st.B_batch, a.st.B_row, e);
+    pb = min(pb, piece_of(a.Cm, a.st.C_batch, a.st.C_row, e));
+    pb = min(pb, piece_of(nullptr, noff, 0, e));
+    const int piece = min(px, pb);
+    if (piece == 16) return launch_scan_piece<T, NS, LANES, 16>(a);
+    if (piece == 4) return launch_scan_piece<T, NS, LANES, 4>(a);
+    if constexpr (sizeof(T) == 2) return launch_scan_piece<T, NS, LANES, 2>(a);
+    return cudaErrorInvalidValue;   // an fp32 element is 4 bytes
 }
 
 template <typename T>
