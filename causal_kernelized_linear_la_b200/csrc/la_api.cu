@@ -591,11 +591,18 @@ la_status la_ssm_conv(const void* x, const float* weight, const float* bias, con
     const size_t e = cfg->dtype == LA_BF16 ? 2 : 4;
     const size_t cache_bytes = (size_t)B * (w - 1) * D * e;
     if (cache_out != cache && la::overlap(cache_out, cache_bytes, cache, cache_bytes)) return LA_ERR_INVALID;
-    if (la::overlap(cache_out, cache_bytes, x, la::extent(B, N, D, x_batch, x_row, e))) return LA_ERR_INVALID;
+    const size_t x_bytes = la::extent(B, N, D, x_batch, x_row, e), out_bytes = (size_t)B * N * D * e;
+    if (la::overlap(cache_out, cache_bytes, x, x_bytes)) return LA_ERR_INVALID;
     const void* rows[] = {x, cache, out, cache_out};
     for (const void* p : rows)
         if (!la::aligned_to(p, e)) return LA_ERR_ALIGN;
     if (!la::aligned16(weight) || !la::aligned16(bias)) return LA_ERR_ALIGN;
+    // a run of tokens reads the rows before it: out in place of x would change them (out may lie
+    // between the batches of a strided x: only a dense one is compared)
+    const bool dense = (x_row == D || N == 1) && (x_batch == (long long)N * D || B == 1);
+    if (dense && N > 0 && la::overlap(out, out_bytes, x, x_bytes)) return LA_ERR_INVALID;
+    if (la::overlap(out, out_bytes, cache, cache_bytes) || la::overlap(out, out_bytes, cache_out, cache_bytes))
+        return LA_ERR_INVALID;
     if (w == 1) cache = cache_out = nullptr;
     if (N == 0 && !cache_out) return LA_OK;
     const int step = la::launch_group(seq_lens);

@@ -21,7 +21,7 @@
 // than a token's rows, is loaded once for them.
 //
 // At 32768 tokens x 4096 channels, bf16, 4 taps, bias and SiLU the prompt kernel
-// takes 97 us (5.5 TB/s; 82 us at the copy rate); with the rows in flight held in
+// takes 94 us (5.7 TB/s; 82 us at the copy rate; 97 and 108 with runs of 64 and 32 tokens); with the rows in flight held in
 // registers it was 120.  Rings of 8 or 12 rows: 105 and 100 us, of 32: 105; two CTAs an
 // SM instead of three: 112, four: 114 (but from five taps on, where three spill, two
 // are faster: eight taps 76 against 144 us at half the tokens); 8 channels a thread
@@ -337,7 +337,7 @@ cudaError_t launch_v(const SsmConvArgs& a)
     }
     // tokens a thread takes: longer runs re-read fewer rows of the history, but
     // threads for two waves of every SM have to be left
-    int run = 64;
+    int run = 128;
     while (run > 2 * kHalf && (long long)a.B * groups * ((a.N + run - 1) / run) < 2 * 148ll * 512) run /= 2;
     const int runs = a.N > 0 ? (a.N + run - 1) / run : 1;
     const long long total = (long long)a.B * groups * runs;

@@ -351,6 +351,7 @@ typedef struct {
  *   out        [B,N,D]; fp32 arithmetic, rounded once.
  *   cache_out  [B,w-1,D] or NULL.  May be the cache itself (updated in place);
  *              any other overlap with cache, and any with x, is LA_ERR_INVALID.
+ *   out shares no byte with the caches, nor with a dense x (LA_ERR_INVALID).
  *   silu       0: act is the identity; 1: act(y) = y / (1 + exp(-y)).
  *   w          1..8.
  *   cfg        dtype and stream are used.

@@ -208,3 +208,10 @@ def test_outputs_that_share_memory_are_refused():
     assert need > 0
     with pytest.raises(ValueError, match="workspace"):        # many bytes by its shape, one in memory
         la.la_ssm_scan(x, x, A, bc, bc, workspace=torch.zeros(1, dtype=torch.uint8).expand(need))
+
+
+def test_conv_out_over_its_inputs():
+    assert _conv(x=P, out=P) == la.LA_ERR_INVALID                              # in place of x
+    assert _conv(x=P, out=P + 128, B=1) == la.LA_ERR_INVALID                   # behind its first rows
+    assert _conv(x=P, out=2 * P, cache=2 * P + 32) == la.LA_ERR_INVALID
+    assert _conv(x=P, out=2 * P, cache_out=2 * P + 32) == la.LA_ERR_INVALID

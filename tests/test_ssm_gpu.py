@@ -281,3 +281,27 @@ def test_refusals():
     assert e.value.code == la.LA_ERR_UNSUPPORTED
     with pytest.raises(ValueError):
         la.la_ssm_step(x[:, 0], x[:, 0], A, bc[:, 0], bc[:, 0], h.bfloat16())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [16, 61])
+def test_scan_rows_of_any_alignment(dtype, n):
+    """How rows reach the kernel does not change a bit: whole 16-byte rows, rows on
+    4 bytes and rows on one element, over more tiles than a kernel holds at once."""
+    N, ch, lens = 700, 1921, [700, 413]
+    p = _scan_inputs(dtype, 2, N, ch, n, 1, True, True, True, True, False, seed=3)
+    assert la.la_ssm_scan_workspace_bytes(2, N, ch, 1, n) == 0
+    fixed = {k: p[k].cuda() for k in ("A", "D", "delta_bias")}
+
+    def rows(t, width, first):
+        base = torch.full((*t.shape[:2], width), float("nan"), dtype=dtype, device="cuda")
+        base[..., first:first + t.shape[-1]] = t.cuda()
+        return base[..., first:first + t.shape[-1]]
+    got = []
+    for width, first in ((1928, 0), (1930, 2), (1927, 3)):
+        x, delta, z = (rows(p[k], width, first) for k in ("x", "delta", "z"))
+        B, C = (rows(p[k].flatten(2), width % 8 + 64, first) for k in ("B", "C"))
+        got.append(la.la_ssm_scan(x, delta, B=B, C=C, z=z, h0=p["h"].cuda(), delta_softplus=True, seq_lens=lens, **fixed))
+    for y, h in got[1:]:
+        assert all(torch.equal(y[b, :t], got[0][0][b, :t]) for b, t in enumerate(lens))
+        assert torch.equal(h, got[0][1])
