@@ -21,11 +21,13 @@
 // than a token's rows, is loaded once for them.
 //
 // At 32768 tokens x 4096 channels, bf16, 4 taps, bias and SiLU the prompt kernel
-// takes 94 us (5.7 TB/s; 82 us at the copy rate; 97 and 108 with runs of 64 and 32 tokens); with the rows in flight held in
-// registers it was 120.  Rings of 8 or 12 rows: 105 and 100 us, of 32: 105; two CTAs an
-// SM instead of three: 112, four: 114 (but from five taps on, where three spill, two
-// are faster: eight taps 76 against 144 us at half the tokens); 8 channels a thread
-// and two CTAs: 104.  One token of 256 sequences takes 4.3 us on the GPU.
+// takes 94 us (5.7 TB/s; 82 us at the copy rate): issue slots are 60 % busy and the
+// rest is waiting between dependent steps.  With the rows in flight held in
+// registers it was 120; runs of 64 and 32 tokens: 97 and 108; rings of 8, 12 and 32
+// rows: 105, 100 and 105; two CTAs an SM instead of three: 112, four: 114 (but from
+// five taps on, where three spill, two are faster: eight taps 76 against 144 us at
+// half the tokens); 8 channels a thread and two CTAs: 104.  One token of 256 sequences
+// takes 4.3 us on the GPU.
 #include "f32x2.cuh"
 #include "la_internal.cuh"
 #include "sm100.cuh"
