@@ -18,6 +18,9 @@
 //   warp 9          MMA issue; describes each key tile to the softmax warps
 //   warp 10         zeroes the value rows of a tile that hold no token: padding
 //                   and unfilled slots may hold NaN, and 0 * NaN is not 0
+// A ring stage is refilled after the products that read it and after warp 10
+// has seen it full: warp 10 follows every load, and a stage that passed two
+// phases under it would look like one that has not been loaded yet.
 // The weights are rounded to bf16 (half a step, 2^-8): the tensor cores take
 // both operands of a product in one type.  l adds the weights before that
 // rounding, in fp32.
@@ -211,7 +214,7 @@ window_prefill_tc(const __grid_constant__ Maps maps, const __grid_constant__ Win
         if (lane == 0) {
             for (int s = 0; s < P::STAGES; ++s) {
                 mbar_init(&full[s], 1);
-                mbar_init(&empty[s], 1);
+                mbar_init(&empty[s], 2);       // the products, and warp 10
             }
             mbar_init(q_full, 1);
             for (int g = 0; g < 2; ++g) {
@@ -380,10 +383,11 @@ window_prefill_tc(const __grid_constant__ Maps maps, const __grid_constant__ Win
         int item = 0, nv = 0;
         for (int it = 0; it < tiles && ok; ++it) {
             if (!active(it, 0) && !active(it, 1)) continue;
-            // every load is waited for in turn, so that no barrier phase is mistaken for another
-            ok = mbar_wait(&full[item % P::STAGES], (item / P::STAGES) & 1, kErrTmaLoad);
+            // every load is waited for in turn, and its stage given back, by the whole warp
+            ok = __all_sync(~0u, mbar_wait(&full[item % P::STAGES], (item / P::STAGES) & 1, kErrTmaLoad));
+            if (ok && lane == 0) mbar_arrive(&empty[item % P::STAGES]);
             ++item;
-            ok = ok && mbar_wait(&full[item % P::STAGES], (item / P::STAGES) & 1, kErrTmaLoad);
+            if (ok) ok = __all_sync(~0u, mbar_wait(&full[item % P::STAGES], (item / P::STAGES) & 1, kErrTmaLoad));
             const int live = w.live(it);
             if (ok && live < kKeys) {
                 unsigned char* vt = sm + P::OFF_RING + (item % P::STAGES) * P::STAGE;
@@ -394,7 +398,10 @@ window_prefill_tc(const __grid_constant__ Maps maps, const __grid_constant__ Win
                 fence_async_smem();
             }
             __syncwarp();
-            if (ok && lane == 0) mbar_arrive(&clean[nv % 3]);
+            if (ok && lane == 0) {
+                mbar_arrive(&clean[nv % 3]);
+                mbar_arrive(&empty[item % P::STAGES]);
+            }
             ++nv;
             ++item;
         }

@@ -171,6 +171,34 @@ def test_prefill_behind_the_cache(dtype, B, Hq, Hkv, N, d, dv, window, sinks, po
     _with_cache(dtype, B, Hq, Hkv, N, d, dv, window, sinks, pos, lens, scale)
 
 
+@pytest.mark.parametrize("N", [40000, 300])
+def test_prefill_behind_a_long_cache(N):
+    """A chunk behind a full cache of 512 tiles: its later queries see none of the
+    hundreds of tiles between the sinks and the window's edge, which every walking
+    warp passes over on its own.  Sampled rows against the definition."""
+    d, window, sinks, pos0 = 64, 65536, 4, 65536 + 4 + 1000      # the ring has wrapped
+    g = torch.Generator(device="cuda").manual_seed(N)
+    r = lambda n: torch.randn(1, 1, n, d, generator=g, device="cuda").bfloat16()  # noqa: E731
+    kh, vh, q = r(pos0 + N), r(pos0 + N), r(N)
+    p = torch.arange(pos0, device="cuda")
+    p = p[(p < sinks) | (p >= pos0 - window)]
+    slot = torch.where(p < sinks, p, sinks + (p - sinks) % window)
+    kc = torch.zeros(1, 1, window + sinks, d, device="cuda", dtype=torch.bfloat16)
+    vc = torch.zeros_like(kc)
+    kc[:, :, slot], vc[:, :, slot] = kh[:, :, p], vh[:, :, p]
+    o = la.la_window_prefill(q, kh[:, :, pos0:], vh[:, :, pos0:], window, sinks=sinks, k_cache=kc, v_cache=vc,
+                             pos=torch.tensor([pos0], dtype=torch.int32, device="cuda"))
+    la.la_prefill_check()
+    o, q, kh, vh = (_f64(t)[0, 0] for t in (o, q, kh, vh))
+    for i in sorted({0, 1, 127, 128, 255, 256, N // 2, N - 257, N - 129, N - 1} & set(range(N))):
+        ref, tol = _ref(q[i:i + 1], kh[:pos0 + i + 1], vh[:pos0 + i + 1], pos0 + i, window, sinks, d ** -0.5, torch.bfloat16)
+        _check(o[i:i + 1], ref, tol, f"query {i}")
+    i = np.arange(pos0, pos0 + N)
+    held = np.concatenate([np.arange(sinks), i[-window:]])
+    at = torch.from_numpy(np.where(held < sinks, held, sinks + (held - sinks) % window)).cuda()
+    assert np.array_equal(_f64(kc)[0, 0][at.cpu()], kh[held]) and np.array_equal(_f64(vc)[0, 0][at.cpu()], vh[held])
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("B,Hq,Hkv,d,dv,window,sinks,pos", [
     (1, 1, 1, 64, 64, 1, 0, [0]),
