@@ -279,8 +279,7 @@ window_prefill_tc(const __grid_constant__ Maps maps, const __grid_constant__ Win
         const bool leader = elect_one();
         bool dead = false;
         auto wait = [&](uint64_t* bar, int phase, unsigned int site) {
-            if (!dead) dead = !mbar_wait(bar, phase & 1, site);
-            __syncwarp();
+            if (!dead) dead = !__all_sync(~0u, mbar_wait(bar, phase & 1, site));
         };
         // a negative scale negates Q (the descriptor's bit 13), so the maximum of the scores is what counts
         const uint32_t id_s = idesc_bf16_f32(kM, kKeys, 0, 0) | (a.scale < 0.f ? 1u << 13 : 0u), id_o = idesc_bf16_f32(kM, DV, 0, 1);
@@ -417,8 +416,10 @@ window_prefill_tc(const __grid_constant__ Maps maps, const __grid_constant__ Win
         const uint32_t ts = tmem_addr(tbase, quad, P::T_S + g * kKeys), to = tmem_addr(tbase, quad, P::T_O + g * DV);
         int n = 0;          // tiles done
         bool ok = true;
+        // a wait that gave up in one lane has given up for the warp: the lanes stay together
+        auto wait = [&](uint64_t* bar, int phase) { return (bool)__all_sync(~0u, mbar_wait(bar, phase & 1, kErrMma)); };
         for (bool last = false; !last; ++n) {
-            if (!mbar_wait(&s_full[g], n & 1, kErrMma)) { ok = false; break; }
+            if (!wait(&s_full[g], n)) { ok = false; break; }
             tc_fence_after();
             const int2 tile = desc[g];
             last = tile.y & kLastTile;
@@ -451,7 +452,7 @@ window_prefill_tc(const __grid_constant__ Maps maps, const __grid_constant__ Win
                 const float f = need && had ? ex2_approx((m - top) * c) : 1.f;
                 if (__any_sync(~0u, need && had)) {
                     // O holds the tiles before this one; a row that has seen nothing holds zeros
-                    if (!mbar_wait(&o_done[g], (n - 1) & 1, kErrMma)) { ok = false; break; }
+                    if (!wait(&o_done[g], n - 1)) { ok = false; break; }
                     tc_fence_after();
 #pragma unroll 1
                     for (int x = 0; x < DV; x += 16) {
@@ -491,7 +492,7 @@ window_prefill_tc(const __grid_constant__ Maps maps, const __grid_constant__ Win
                 }
             }
         }
-        if (ok && mbar_wait(&o_done[g], (n - 1) & 1, kErrMma)) {
+        if (ok && wait(&o_done[g], n - 1)) {
             tc_fence_after();
             const float2 l1 = unpack2(add2(l[0], l[1]));
             const float inv = 1.f / (l1.x + l1.y);     // every query sees itself
