@@ -3,6 +3,7 @@
 #include <stdint.h>
 
 #include "la_internal.cuh"
+#include "la_overlap.cuh"
 #include "la_prefill_tc.cuh"
 #include "la_window.cuh"
 
@@ -250,13 +251,6 @@ SsmArgs ssm_from(SsmArgs a, int b0, int count)
 
 // ---- sliding-window attention --------------------------------------------------
 
-// Bytes from the first to past the last element of a [B, H, N, cols] tensor.
-size_t extent4(int B, int H, int N, int cols, long long batch, long long head, long long row, size_t e)
-{
-    if (B <= 0 || H <= 0 || N <= 0) return 0;
-    return ((size_t)(B - 1) * batch + (size_t)(H - 1) * head + (size_t)(N - 1) * row + cols) * e;
-}
-
 // Checks shared by la_window_prefill and la_window_decode_step (N = 1); fills the arguments.
 la_status check_window(WindowArgs* w, const void* q, const void* k, const void* v, void* out, void* k_cache,
                        void* v_cache, const int* pos, int B, int Hq, int Hkv, int N, int d, int dv, int window,
@@ -295,18 +289,27 @@ la_status check_window(WindowArgs* w, const void* q, const void* k, const void* 
     // nor do two heads or sequences of out
     if (work > 0 && ((Hq > 1 && s.out_head == 0) || (B > 1 && s.out_batch == 0))) return LA_ERR_INVALID;
     if (work > 0) {
-        const size_t cap = (size_t)window + sinks;
-        const size_t ks = extent4(B, Hkv, N, d, s.k_batch, s.k_head, s.k_row, e);
-        const size_t vs = extent4(B, Hkv, N, dv, s.v_batch, s.v_head, s.v_row, e);
-        const size_t os = extent4(B, Hq, N, dv, s.out_batch, s.out_head, s.out_row, e);
-        const void* written[] = {out, k_cache, v_cache};
-        const size_t wn[] = {os, (size_t)B * Hkv * cap * d * e, (size_t)B * Hkv * cap * dv * e};
+        const Region rq = region(q, e, d, {B, Hq, N}, {s.q_batch, s.q_head, s.q_row});
+        const Region rk = region(k, e, d, {B, Hkv, N}, {s.k_batch, s.k_head, s.k_row});
+        const Region rv = region(v, e, dv, {B, Hkv, N}, {s.v_batch, s.v_head, s.v_row});
+        const Region ro = region(out, e, dv, {B, Hq, N}, {s.out_batch, s.out_head, s.out_row});
+        const size_t slots = (size_t)B * Hkv * ((size_t)window + sinks);
+        const Region rkc = dense(k_cache, slots * d * e), rvc = dense(v_cache, slots * dv * e);
+        const Region rp = dense(pos, (size_t)B * sizeof(int));
+        if (overlaps_itself(ro)) return LA_ERR_INVALID;
+        // blocks read k and v, positions and caches while others write; q's rows are read by the block
+        // that writes the same rows of out alone, so out may take q's place, but not a shifted one
+        auto alike = [](int count, long long x, long long y) { return count == 1 || x == y; };
+        const bool in_place = out == q && dv == d && alike(B, s.q_batch, s.out_batch) && alike(Hq, s.q_head, s.out_head) &&
+                              alike(N, s.q_row, s.out_row);
+        if (!in_place && shared(ro, rq)) return LA_ERR_INVALID;
+        const Region* written[] = {&ro, &rkc, &rvc};
         for (int i = 0; i < 3; ++i) {
-            // strided k and v may interleave with a strided out inside one buffer: only dense ranges are compared
-            if (!st && (overlap(written[i], wn[i], k, ks) || overlap(written[i], wn[i], v, vs))) return LA_ERR_INVALID;
-            if (i > 0 && (overlap(written[i], wn[i], k, ks) || overlap(written[i], wn[i], v, vs))) return LA_ERR_INVALID;
+            for (const Region* r : {&rk, &rv, &rp})
+                if (shared(*written[i], *r)) return LA_ERR_INVALID;
+            if (i > 0 && (shared(*written[i], rq) || shared(*written[i], ro))) return LA_ERR_INVALID;
         }
-        if (overlap(k_cache, wn[1], v_cache, wn[2])) return LA_ERR_INVALID;
+        if (shared(rkc, rvc)) return LA_ERR_INVALID;
     }
     *w = WindowArgs{};
     w->q = q; w->k = k; w->v = v; w->out = out; w->k_cache = k_cache; w->v_cache = v_cache; w->pos = pos;

@@ -427,6 +427,9 @@ LA_API la_status la_ssm_step(const void* x, const void* delta, const float* A, c
  * sinks + window < 2^30 (LA_ERR_UNSUPPORTED); positions stay below 2^31; rows of
  * one head are at least d (dv) elements apart; several query heads or sequences
  * may read one head of q, k or v (stride 0), but each has its own rows of out.
+ * out and the caches share no byte with another argument (LA_ERR_INVALID), but
+ * out may be q itself (same address and strides, dv = d), and rows of out may lie
+ * between those of a strided q, k or v.
  * Sums, maxima and outputs accumulate in fp32.  All pointers are 16-byte
  * aligned, and so are the rows (strides are multiples of 16 bytes).
  */
@@ -459,8 +462,7 @@ typedef struct {
  * bf16 runs on the tensor cores and rounds the weights w_ij (relative to the
  * row's running reference) to bf16; fp32 keeps fp32 arithmetic throughout.
  * One kernel, and with a cache a second one that moves the tokens into it.
- * LA_ERR_INVALID, LA_ERR_UNSUPPORTED, LA_ERR_ALIGN as elsewhere; LA_ERR_INVALID
- * too if a cache, or a dense out, overlaps k or v.
+ * LA_ERR_INVALID, LA_ERR_UNSUPPORTED, LA_ERR_ALIGN as elsewhere.
  */
 LA_API la_status la_window_prefill(const void* q, const void* k, const void* v, void* out,
                                    void* k_cache, void* v_cache, const int* pos, const int* seq_lens,

@@ -215,3 +215,37 @@ def test_conv_out_over_its_inputs():
     assert _conv(x=P, out=P + 128, B=1) == la.LA_ERR_INVALID                   # behind its first rows
     assert _conv(x=P, out=2 * P, cache=2 * P + 32) == la.LA_ERR_INVALID
     assert _conv(x=P, out=2 * P, cache_out=2 * P + 32) == la.LA_ERR_INVALID
+
+
+def test_window_outputs_over_other_arguments():
+    """The layout decides, not whether strides are given: the binding always gives them."""
+    bad = la.LA_ERR_INVALID
+    dense = LaWindowStrides(1024, 512, 64, 512, 512, 64, 512, 512, 64, 1024, 512, 64)
+    for st in (None, dense):
+        assert _window(out=2 * P + 64, st=st) == bad                # over k
+        assert _window(out=3 * P - 64, st=st) == bad                # its last rows over v's first
+        assert _window(out=P + 128, st=st) == bad                   # over q, a row on
+        assert _window(kc=FAR, vc=FAR << 1, out=FAR + 128, st=st) == bad
+        assert _window(kc=FAR, vc=FAR << 1, out=(FAR << 1) + 128, st=st) == bad
+        assert _window(kc=FAR, vc=FAR << 1, q=FAR, st=st) == bad    # q inside a cache
+        assert _window(kc=FAR, vc=FAR << 1, pos=4 * P + 16, st=st) == bad      # positions inside out
+        assert _window(kc=FAR, vc=FAR << 1, pos=FAR + 16, st=st) == bad        # ... inside a cache
+    # out over q with another order of rows and heads
+    assert _window(out=P, st=LaWindowStrides(1024, 512, 64, 512, 512, 64, 512, 512, 64, 1024, 64, 128)) == bad
+    # heads (sequences) of out that are neither equal nor apart
+    assert _window(st=LaWindowStrides(1024, 512, 64, 512, 512, 64, 512, 512, 64, 1024, 8, 64)) == bad
+    assert _window(B=2, st=LaWindowStrides(1024, 512, 64, 512, 512, 64, 512, 512, 64, 64, 512, 64)) == bad
+    # one buffer of 8 rows of 64 x (2 q, 1 k, 1 v): out on k's columns
+    packed = LaWindowStrides(2048, 64, 256, 2048, 64, 256, 2048, 64, 256, 2048, 64, 256)
+    assert _window(q=P, k=P + 256, v=P + 384, out=P + 128, st=packed) == bad
+
+
+def test_decode_outputs_over_other_arguments():
+    def call(q=P, out=4 * P, pos=5 * P, Hq=2, st=None):
+        c = _cfg()
+        return la.lib().la_window_decode_step(C(q), C(2 * P), C(3 * P), C(out), C(FAR), C(FAR << 1), C(pos), 1, Hq, 1, 64,
+                                              64, 4, 1, 0.1, None if st is None else ctypes.byref(st), ctypes.byref(c))
+    for st in (None, LaWindowStrides(128, 64, 0, 64, 64, 0, 64, 64, 0, 128, 64, 0)):
+        for kw in (dict(out=2 * P), dict(out=3 * P - 128), dict(out=FAR + 128), dict(out=(FAR << 1) + 512), dict(q=FAR),
+                   dict(out=P + 128), dict(pos=FAR), dict(pos=4 * P + 16)):
+            assert call(st=st, **kw) == la.LA_ERR_INVALID, kw

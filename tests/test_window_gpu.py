@@ -275,3 +275,50 @@ def test_refusals():
         la.la_window_decode_step(q[:, :, 0], k[:, :, 0], k[:, :, 0], kc, vc, pos.long(), 16, sinks=4)
     with pytest.raises(ValueError):
         la.la_window_decode_step(q[:, :, 0], k[:, :, 0], k[:, :, 0], kc, vc, pos.cpu(), 16, sinks=4)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_outputs_beside_and_over_q(dtype):
+    """out as a part of the buffer that q, k and v are parts of, and out in q's place:
+    the bits of an out of its own."""
+    B, N, H, Hkv, d, window, sinks, lens = 2, 300, 4, 2, 64, 70, 3, [300, 111]
+    g = torch.Generator().manual_seed(21)
+    base = torch.randn(B, N, 2 * H + 2 * Hkv, d, generator=g).to(dtype).cuda()
+
+    def parts(t):
+        t = t.transpose(1, 2)
+        return t[:, :H], t[:, H:H + Hkv], t[:, H + Hkv:H + 2 * Hkv], t[:, H + 2 * Hkv:]
+    q, k, v, _ = parts(base)
+    want = torch.full((B, H, N, d), 7.0, dtype=dtype, device="cuda")
+    la.la_window_prefill(q, k, v, window, sinks=sinks, seq_lens=lens, out=want)
+    one = base.clone()
+    q1, k1, v1, o1 = parts(one)
+    o1.fill_(7.0)
+    la.la_window_prefill(q1, k1, v1, window, sinks=sinks, seq_lens=lens, out=o1)
+    assert torch.equal(o1, want) and all(torch.equal(x, y) for x, y in zip((q1, k1, v1), (q, k, v)))
+    two = base.clone()
+    q2, k2, v2, _ = parts(two)
+    la.la_window_prefill(q2, k2, v2, window, sinks=sinks, seq_lens=lens, out=q2)
+    for b, n in enumerate(lens):
+        assert torch.equal(q2[b, :, :n], want[b, :, :n]) and torch.equal(q2[b, :, n:], q[b, :, n:])
+    # one token, q's heads over several CTAs of a cluster
+    cap = 2000
+    kc, vc = torch.randn(B, Hkv, cap, d, generator=g).to(dtype).cuda(), torch.randn(B, Hkv, cap, d, generator=g).to(dtype).cuda()
+    pos = torch.tensor([5000, 70], dtype=torch.int32, device="cuda")
+    q1, k1, v1 = q[:, :, 0].contiguous(), k[:, :, 0].contiguous(), v[:, :, 0].contiguous()
+    kc2, vc2 = kc.clone(), vc.clone()
+    want = la.la_window_decode_step(q1, k1, v1, kc, vc, pos, cap - 4, sinks=4)
+    got = la.la_window_decode_step(q1, k1, v1, kc2, vc2, pos, cap - 4, sinks=4, out=q1)
+    assert got is q1 and torch.equal(q1, want)
+    la.la_prefill_check()
+    # out over k, over a cache, over rows of q that are not its own: refused, nothing written
+    keep = two.clone()
+    for out in (two.transpose(1, 2)[:, 1:1 + H], two.transpose(1, 2)[:, H:2 * H]):
+        with pytest.raises(la.LaError) as e:
+            la.la_window_prefill(q2, k2, v2, window, sinks=sinks, out=out)
+        assert e.value.code == la.LA_ERR_INVALID
+    with pytest.raises(la.LaError) as e:
+        la.la_window_decode_step(want, k1, v1, kc, vc, pos, cap - 4, sinks=4, out=kc.view(-1)[:B * H * d].view(B, H, d))
+    assert e.value.code == la.LA_ERR_INVALID
+    torch.cuda.synchronize()
+    assert torch.equal(two, keep)
