@@ -228,6 +228,34 @@ SsmArgs ssm_args(const void* x, const void* delta, const float* A, const void* B
     return a;
 }
 
+// Blocks read the inputs while others write out, the states (h) and the summaries of the workspace: none of
+// these shares a byte with another argument.  But out may be x, delta or z: a block reads the rows of its
+// channels before it writes them, and no other block reads them.
+bool ssm_shares(const SsmArgs& a, const float* h0, const void* workspace, size_t workspace_bytes)
+{
+    const size_t e = a.dtype == LA_BF16 ? 2 : 4, states = (size_t)a.B * a.D * a.n * sizeof(float);
+    const size_t channels = (size_t)a.D * sizeof(float);
+    auto rows = [&](const void* p, long long cols, long long batch, long long row) {
+        return region(p, e, cols, {a.B, a.N, 1}, {batch, row, 0});
+    };
+    auto out_is = [&](const void* p, long long batch, long long row) {
+        return p == a.out && (a.B == 1 || batch == (long long)a.N * a.D) && (a.N == 1 || row == a.D);
+    };
+    const long long bc = (long long)a.G * a.n;
+    const la_ssm_strides& st = a.st;
+    const Region in[] = {rows(a.x, a.D, st.x_batch, st.x_row), rows(a.delta, a.D, st.delta_batch, st.delta_row),
+                         rows(a.z, a.D, st.z_batch, st.z_row), rows(a.Bm, bc, st.B_batch, st.B_row),
+                         rows(a.Cm, bc, st.C_batch, st.C_row), dense(a.A, channels * a.n), dense(a.skip, channels),
+                         dense(a.delta_bias, channels), dense(h0, states)};
+    const bool in_place[] = {out_is(a.x, st.x_batch, st.x_row), out_is(a.delta, st.delta_batch, st.delta_row),
+                             out_is(a.z, st.z_batch, st.z_row)};
+    const Region out = rows(a.out, a.D, (long long)a.N * a.D, a.D), h = dense(a.h_out, states),
+                 ws = dense(workspace, workspace_bytes);
+    for (int i = 0; i < 9; ++i)
+        if ((!(i < 3 && in_place[i]) && shared(out, in[i])) || shared(h, in[i]) || shared(ws, in[i])) return true;
+    return shared(out, h) || shared(out, ws) || shared(h, ws);
+}
+
 // The sequences from b0 on of a batch's arguments.
 SsmArgs ssm_from(SsmArgs a, int b0, int count)
 {
@@ -652,20 +680,22 @@ la_status la_ssm_scan(const void* x, const void* delta, const float* A, const vo
     if (!la::lens_ok(seq_lens, B, N)) return LA_ERR_INVALID;
     const size_t states = (size_t)B * D * n * sizeof(float);
     if (la::overlap(h_out, states, cfg->S0, states)) return LA_ERR_INVALID;
-    if (cfg->workspace_bytes < la_ssm_scan_workspace_bytes(B, N, D, G, n)) return LA_ERR_WORKSPACE;
+    const size_t need = la_ssm_scan_workspace_bytes(B, N, D, G, n);
+    if (cfg->workspace_bytes < need || (need > 0 && !cfg->workspace)) return LA_ERR_WORKSPACE;
     if (B == 0 || D == 0) return LA_OK;
+    la::SsmArgs all = la::ssm_args(x, delta, A, Bm, Cm, D_skip, z, delta_bias, out, h_out, B, N, D, G, n,
+                                   delta_softplus, strides, cfg);
+    if (la::ssm_shares(all, cfg->S0, cfg->workspace, need)) return LA_ERR_INVALID;
     cudaStream_t stream = static_cast<cudaStream_t>(cfg->stream);
     if (N == 0) {
         if (!h_out) return LA_OK;
         return la::from_cuda(cfg->S0 ? cudaMemcpyAsync(h_out, cfg->S0, states, cudaMemcpyDeviceToDevice, stream)
                                      : cudaMemsetAsync(h_out, 0, states, stream));
     }
-    la::SsmArgs all = la::ssm_args(x, delta, A, Bm, Cm, D_skip, z, delta_bias, out, h_out, B, N, D, G, n,
-                                   delta_softplus, strides, cfg);
     all.h0 = cfg->S0;
     all.seq_lens = seq_lens;
     la::ssm_scan_segments(B, N, D, G, n, &all.segs, &all.seg_len);
-    const size_t per = la_ssm_scan_workspace_bytes(B, N, D, G, n) / B / sizeof(float);
+    const size_t per = need / B / sizeof(float);
     const int step = la::launch_group(seq_lens);
     for (int b0 = 0; b0 < B; b0 += step) {
         la::SsmArgs a = la::ssm_from(all, b0, B - b0 < step ? B - b0 : step);
@@ -684,8 +714,10 @@ la_status la_ssm_step(const void* x, const void* delta, const float* A, const vo
     if (st != LA_OK) return st;
     if (B == 0 || D == 0) return LA_OK;
     if (!h) return LA_ERR_INVALID;
-    return la::from_cuda(la::launch_ssm_step(
-        la::ssm_args(x, delta, A, Bm, Cm, D_skip, z, delta_bias, out, h, B, 1, D, G, n, delta_softplus, strides, cfg)));
+    const la::SsmArgs a =
+        la::ssm_args(x, delta, A, Bm, Cm, D_skip, z, delta_bias, out, h, B, 1, D, G, n, delta_softplus, strides, cfg);
+    if (la::ssm_shares(a, nullptr, nullptr, 0)) return LA_ERR_INVALID;
+    return la::from_cuda(la::launch_ssm_step(a));
 }
 
 la_status la_window_prefill(const void* q, const void* k, const void* v, void* out, void* k_cache, void* v_cache,

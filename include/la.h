@@ -377,8 +377,11 @@ LA_API la_status la_ssm_conv(const void* x, const float* weight, const float* bi
  *   out        y [B,N,D].
  *   h_out      final states [B,D,n] fp32 or NULL; a sequence of length 0 reports its start state.
  *   cfg        dtype, stream; S0 = start states [B,D,n] fp32 or NULL (zero);
- *              workspace of la_ssm_scan_workspace_bytes() bytes.  h_out must not
- *              share a byte with S0 (LA_ERR_INVALID): alternate two buffers.
+ *              workspace of la_ssm_scan_workspace_bytes() bytes.
+ *
+ * out, h_out and the workspace share no byte with another argument
+ * (LA_ERR_INVALID; for h_out and S0 alternate two buffers), but out may be x,
+ * delta or z itself (same address, dense).
  *
  * All arithmetic is fp32.  LA_ERR_INVALID, LA_ERR_UNSUPPORTED (n > 64),
  * LA_ERR_ALIGN, LA_ERR_WORKSPACE as elsewhere.
@@ -399,6 +402,9 @@ LA_API size_t la_ssm_scan_workspace_bytes(int B, int N, int D, int G, int n);
  *
  *   h          [B,D,n] fp32, read and updated in place.
  *   cfg        dtype and stream are used.
+ *
+ * out and h share no byte with another argument (LA_ERR_INVALID), but out may
+ * be x, delta or z itself.
  */
 LA_API la_status la_ssm_step(const void* x, const void* delta, const float* A, const void* Bm, const void* Cm,
                              const float* D_skip, const void* z, const float* delta_bias, float* h, void* out,

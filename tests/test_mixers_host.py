@@ -249,3 +249,52 @@ def test_decode_outputs_over_other_arguments():
         for kw in (dict(out=2 * P), dict(out=3 * P - 128), dict(out=FAR + 128), dict(out=(FAR << 1) + 512), dict(q=FAR),
                    dict(out=P + 128), dict(pos=FAR), dict(pos=4 * P + 16)):
             assert call(st=st, **kw) == la.LA_ERR_INVALID, kw
+
+
+def _ssm(step, x=P, delta=2 * P, A=3 * P, Bm=4 * P, Cm=5 * P, D=6 * P, z=7 * P, bias=8 * P, out=9 * P, h=10 * P, S0=None,
+         ws=None, wsb=0, N=40, st=None):
+    B, ch, G, n = 2, 32, 1, 16
+    c = _cfg(S0=S0, ws=ws, wsb=wsb)
+    st = None if st is None else ctypes.byref(st)
+    ptrs = [C(p) for p in (x, delta, A, Bm, Cm, D, z, bias)]
+    if step:
+        return la.lib().la_ssm_step(*ptrs, C(h), C(out), B, ch, G, n, 1, st, ctypes.byref(c))
+    return la.lib().la_ssm_scan(*ptrs, C(out), C(h), None, B, N, ch, G, n, 1, st, ctypes.byref(c))
+
+
+@pytest.mark.parametrize("step", [False, True])
+def test_ssm_outputs_over_other_arguments(step):
+    """Two sequences of 32 channels and 16 states: rows of 64 bytes, states of 2048 bytes a sequence."""
+    bad = la.LA_ERR_INVALID
+    for arg in ("Bm", "Cm", "A", "D", "bias", "h"):
+        at = dict(Bm=4, Cm=5, A=3, D=6, bias=8, h=10)[arg] * P
+        assert _ssm(step, out=at) == bad, arg                       # out over it ...
+        assert _ssm(step, out=at - 64) == bad, arg                  # ... by its last row
+        if arg != "h":
+            assert _ssm(step, h=at) == bad, arg
+            assert _ssm(step, h=at - 4080) == bad, arg
+    for arg in ("x", "delta", "z"):
+        at = dict(x=1, delta=2, z=7)[arg] * P
+        assert _ssm(step, out=at + 64) == bad, arg                  # a row on
+        assert _ssm(step, out=at - 2) == bad, arg
+        assert _ssm(step, h=at) == bad, arg
+    # in x's place, but x has other strides
+    wide = LaSsmStrides(80 * 32, 64, 40 * 32, 32, 40 * 32, 32, 40 * 16, 16, 40 * 16, 16)
+    assert _ssm(step, out=P, st=wide) == bad
+    # every sequence reads the first one's rows, out has rows of its own
+    one = LaSsmStrides(0, 32, 40 * 32, 32, 40 * 32, 32, 40 * 16, 16, 40 * 16, 16)
+    assert _ssm(step, out=P, st=one) == bad
+
+
+def test_scan_workspace_over_other_arguments():
+    N = 4096
+    need = la.la_ssm_scan_workspace_bytes(2, N, 32, 1, 16)
+    assert need > 0
+    far = 1 << 40
+    assert _ssm(False, N=N, ws=None, wsb=need) == la.LA_ERR_WORKSPACE          # bytes of no workspace
+    apart = dict(x=far, delta=2 * far, A=3 * far, Bm=4 * far, Cm=5 * far, D=6 * far, z=7 * far, bias=8 * far, out=9 * far,
+                 h=10 * far, S0=11 * far)
+    for arg, at in apart.items():
+        assert _ssm(False, N=N, **apart, ws=at, wsb=need) == la.LA_ERR_INVALID, arg
+        assert _ssm(False, N=N, **apart, ws=at - need + 16, wsb=need) == la.LA_ERR_INVALID, arg
+    assert _ssm(False, N=N, **{**apart, "S0": apart["out"] + 64}, ws=far // 2, wsb=need) == la.LA_ERR_INVALID

@@ -305,3 +305,36 @@ def test_scan_rows_of_any_alignment(dtype, n):
     for y, h in got[1:]:
         assert all(torch.equal(y[b, :t], got[0][0][b, :t]) for b, t in enumerate(lens))
         assert torch.equal(h, got[0][1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,N,ch,n,G,lens", [
+    (2, 1500, 64, 16, 2, [1500, 700]),     # several segments
+    (1, 300, 1921, 5, 1, None),            # rows off 4 bytes
+    (1, 200, 2048, 16, 1, None),
+])
+def test_out_in_an_inputs_place(dtype, B, N, ch, n, G, lens):
+    """out may be x, delta or z itself: the bits of an out of its own, for prompts and tokens."""
+    p = {k: _view_cuda(v) for k, v in _scan_inputs(dtype, B, N, ch, n, G, True, True, True, True, False, seed=N).items()}
+    assert (la.la_ssm_scan_workspace_bytes(B, N, ch, G, n) > 0) == (N == 1500)
+
+    def scan(out, q):
+        return la.la_ssm_scan(q["x"], q["delta"], q["A"], q["B"], q["C"], D=q["D"], z=q["z"], delta_bias=q["delta_bias"],
+                              delta_softplus=True, h0=q["h"], seq_lens=lens, out=out)
+
+    def step(out, q):
+        h = q["h"].clone()
+        return la.la_ssm_step(*(q[k][:, 0] if k != "A" else q[k] for k in ("x", "delta", "A", "B", "C")), h, D=q["D"],
+                              z=q["z"][:, 0], delta_bias=q["delta_bias"], delta_softplus=True, out=out), h
+    want = scan(torch.zeros(B, N, ch, dtype=dtype, device="cuda"), p)
+    want1 = step(torch.zeros(B, ch, dtype=dtype, device="cuda"), p)
+    for name in ("x", "delta", "z"):
+        q = {**p, name: p[name].clone()}
+        y, h = scan(q[name], q)
+        for b in range(B):
+            m = N if lens is None else lens[b]
+            assert torch.equal(y[b, :m], want[0][b, :m]) and torch.equal(y[b, m:], p[name][b, m:])
+        assert y is q[name] and torch.equal(h, want[1])
+        q = {**p, name: p[name][:, :1].clone()}
+        got = step(q[name][:, 0], q)
+        assert torch.equal(got[0], want1[0]) and torch.equal(got[1], want1[1])
