@@ -172,13 +172,6 @@ bool lens_ok(const int* lens, int B, int N)
     return true;
 }
 
-// Bytes from the first to past the last element of a [B, N, cols] tensor with these strides.
-size_t extent(int B, int N, long long cols, long long batch, long long row, size_t e)
-{
-    if (B <= 0 || N <= 0 || cols <= 0) return 0;
-    return ((size_t)(B - 1) * batch + (size_t)(N - 1) * row + cols) * e;
-}
-
 // Tokens of a state-space call's sequences: token numbers add up inside 32 bits.
 constexpr int kMostRows = 1 << 30;
 
@@ -620,20 +613,19 @@ la_status la_ssm_conv(const void* x, const float* weight, const float* bias, con
     if (B == 0 || D == 0) return LA_OK;
     if (N > 0 && (!x || !weight || !out)) return LA_ERR_INVALID;
     const size_t e = cfg->dtype == LA_BF16 ? 2 : 4;
-    const size_t cache_bytes = (size_t)B * (w - 1) * D * e;
-    if (cache_out != cache && la::overlap(cache_out, cache_bytes, cache, cache_bytes)) return LA_ERR_INVALID;
-    const size_t x_bytes = la::extent(B, N, D, x_batch, x_row, e), out_bytes = (size_t)B * N * D * e;
-    if (la::overlap(cache_out, cache_bytes, x, x_bytes)) return LA_ERR_INVALID;
     const void* rows[] = {x, cache, out, cache_out};
     for (const void* p : rows)
         if (!la::aligned_to(p, e)) return LA_ERR_ALIGN;
     if (!la::aligned16(weight) || !la::aligned16(bias)) return LA_ERR_ALIGN;
-    // a run of tokens reads the rows before it: out in place of x would change them (out may lie
-    // between the batches of a strided x: only a dense one is compared)
-    const bool dense = (x_row == D || N == 1) && (x_batch == (long long)N * D || B == 1);
-    if (dense && N > 0 && la::overlap(out, out_bytes, x, x_bytes)) return LA_ERR_INVALID;
-    if (la::overlap(out, out_bytes, cache, cache_bytes) || la::overlap(out, out_bytes, cache_out, cache_bytes))
-        return LA_ERR_INVALID;
+    // a run of tokens reads the rows before it, so out in place of x would change them; the caches may be one,
+    // since a thread reads all it needs of them before it writes
+    const size_t cache_bytes = (size_t)B * (w - 1) * D * e;
+    const la::Region rx = la::region(x, e, D, {B, N, 1}, {x_batch, x_row, 0}), rw = la::dense(weight, (size_t)D * w * 4),
+                     rb = la::dense(bias, (size_t)D * 4), rc = la::dense(cache, cache_bytes),
+                     ro = la::dense(out, (size_t)B * N * D * e), rn = la::dense(cache_out, cache_bytes);
+    for (const la::Region* r : {&rx, &rw, &rb})
+        if (la::shared(ro, *r) || la::shared(rn, *r)) return LA_ERR_INVALID;
+    if (la::shared(ro, rc) || la::shared(ro, rn) || (cache_out != cache && la::shared(rc, rn))) return LA_ERR_INVALID;
     if (w == 1) cache = cache_out = nullptr;
     if (N == 0 && !cache_out) return LA_OK;
     const int step = la::launch_group(seq_lens);

@@ -350,8 +350,9 @@ typedef struct {
  *   cache      [B,w-1,D] previous inputs, or NULL for zero history.
  *   out        [B,N,D]; fp32 arithmetic, rounded once.
  *   cache_out  [B,w-1,D] or NULL.  May be the cache itself (updated in place);
- *              any other overlap with cache, and any with x, is LA_ERR_INVALID.
- *   out shares no byte with the caches, nor with a dense x (LA_ERR_INVALID).
+ *              any other overlap with cache is LA_ERR_INVALID.
+ *   out and cache_out share no byte with each other, x, weight or bias, and out
+ *   none with cache (LA_ERR_INVALID); they may lie between the rows of a strided x.
  *   silu       0: act is the identity; 1: act(y) = y / (1 + exp(-y)).
  *   w          1..8.
  *   cfg        dtype and stream are used.

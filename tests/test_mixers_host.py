@@ -298,3 +298,18 @@ def test_scan_workspace_over_other_arguments():
         assert _ssm(False, N=N, **apart, ws=at, wsb=need) == la.LA_ERR_INVALID, arg
         assert _ssm(False, N=N, **apart, ws=at - need + 16, wsb=need) == la.LA_ERR_INVALID, arg
     assert _ssm(False, N=N, **{**apart, "S0": apart["out"] + 64}, ws=far // 2, wsb=need) == la.LA_ERR_INVALID
+
+
+def test_conv_outputs_over_a_strided_x():
+    bad = la.LA_ERR_INVALID
+    # one sequence of 8 rows of 16 in rows of 64 elements: out (256 bytes) over some of them
+    for at in (P, P + 128, P + 2 * 7 * 64 - 224, P - 240):
+        assert _conv(out=at, w_=2 * P, xt=64) == bad
+    # two sequences 1024 elements apart: out over the second, or cache_out over its last row
+    assert _conv(B=2, out=P + 2 * (1024 + 7 * 64), w_=2 * P, xt=64, xb=1024) == bad
+    assert _conv(B=2, out=3 * P, cache_out=P + 2 * (1024 + 7 * 64) + 30, w_=2 * P, xt=64, xb=1024) == bad
+    # the filter and the bias are read by every thread
+    assert _conv(x=4 * P, out=P + 128, w_=P) == bad
+    assert _conv(x=4 * P, out=P + 32, w_=2 * P, bias=P) == bad
+    assert _conv(x=4 * P, out=5 * P, w_=P, cache_out=P + 240) == bad
+    assert _conv(x=4 * P, out=5 * P, w_=2 * P, bias=P, cache_out=P + 32) == bad

@@ -338,3 +338,27 @@ def test_out_in_an_inputs_place(dtype, B, N, ch, n, G, lens):
         q = {**p, name: p[name][:, :1].clone()}
         got = step(q[name][:, 0], q)
         assert torch.equal(got[0], want1[0]) and torch.equal(got[1], want1[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_conv_outputs_between_the_rows_of_x(dtype):
+    """One buffer of a sequence's rows, the output of the sequence, its cache: the bits of buffers of their own."""
+    B, N, D, w = 1, 50, 24, 4
+    g = torch.Generator().manual_seed(4)
+    wt = torch.randn(D, w, generator=g).cuda()
+    base = torch.randn(2 * N * D + 3 * D + N, generator=g).to(dtype).cuda()
+    x = base[:N * D].view(1, N, D)
+    out, cache = base[N * D:2 * N * D].view(1, N, D), base[2 * N * D:2 * N * D + 3 * D].view(1, 3, D)
+    keep, want = base.clone(), la.la_ssm_conv(x.clone(), wt, cache=cache.clone())
+    la.la_ssm_conv(x, wt, cache=cache, out=out, cache_out=cache)
+    assert torch.equal(out, want[0]) and torch.equal(cache, want[1]) and torch.equal(x, keep[:N * D].view(1, N, D))
+    # two sequences far apart, out in the gap behind the first one
+    far = torch.randn(2, 2 * (N * D) + 8 * D, generator=g).to(dtype).cuda()
+    x = far[:, :N * D].view(2, N, D)
+    gap = far.view(-1)[N * D:N * D + 2 * 10 * D].view(2, 10, D)
+    want = la.la_ssm_conv(x[:, 3:13].clone(), wt)
+    got = la.la_ssm_conv(x[:, 3:13], wt, out=gap)
+    assert torch.equal(got[0], want[0])
+    with pytest.raises(la.LaError) as e:
+        la.la_ssm_conv(x, wt, out=far.view(-1)[:2 * N * D].view(2, N, D))
+    assert e.value.code == la.LA_ERR_INVALID
