@@ -241,7 +241,8 @@ window_decode_mma(const __grid_constant__ WindowArgs a, int chunks)
     const float sl = a.scale * kLog2e;
 
     uint4 kr[2][KS], vr[4][VC];
-    // slots past the run repeat its last one, whose values are finite; their weights are zero
+    // slots past the run repeat its last one; their weights are zero, and so are their values by the time
+    // they are used: the last slot's may be infinite
     auto k_row = [&](int s) { const int x = min(s, s1 - 1); return (x == slot_new ? kn : kc + (size_t)x * D) + 8 * t; };
     auto v_row = [&](int s) { const int x = min(s, s1 - 1); return (x == slot_new ? vn : vc + (size_t)x * DV) + 8 * g; };
     auto load_k = [&](int s) {
@@ -333,6 +334,13 @@ window_decode_mma(const __grid_constant__ WindowArgs a, int chunks)
             c[j] = exp2f(c[j] - ref);
             c[2 + j] = exp2f(c[2 + j] - ref);
             l[j] += c[j] + c[2 + j];
+        }
+        if (s + 16 > s1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (s + 2 * t + (i & 1) + 8 * (i >> 1) >= s1)
+#pragma unroll
+                    for (int x = 0; x < VC; ++x) vr[i][x] = make_uint4(0u, 0u, 0u, 0u);
         }
         const uint32_t p0 = transpose8(bf16_pair(c[0], c[1])), p1 = transpose8(bf16_pair(c[2], c[3]));
 #pragma unroll

@@ -322,3 +322,24 @@ def test_outputs_beside_and_over_q(dtype):
     assert e.value.code == la.LA_ERR_INVALID
     torch.cuda.synchronize()
     assert torch.equal(two, keep)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cap,pos", [(44, 30), (44, 43), (44, 200), (1500, 700), (1500, 9000)])
+def test_decode_infinite_value_in_the_last_slot(dtype, cap, pos):
+    """An infinite value that the token sees makes its column of the output infinite, with
+    its sign, and no other: also in the last slot in use, which ends inside a block of slots."""
+    B, Hq, Hkv, d, sinks = 1, 8, 2, 64, 4
+    g = torch.Generator().manual_seed(cap + pos)
+    r = lambda *s: (0.3 * torch.randn(*s, generator=g)).to(dtype).cuda()  # noqa: E731
+    q, k, v, kc, vc = r(B, Hq, d), r(B, Hkv, d), r(B, Hkv, d), r(B, Hkv, cap, d), r(B, Hkv, cap, d)
+    window, used = cap - sinks, min(pos + 1, cap)
+    posd = torch.tensor([pos], dtype=torch.int32, device="cuda")
+    want = la.la_window_decode_step(q, k, v, kc.clone(), vc.clone(), posd, window, sinks=sinks)
+    last = v if _slot(pos, window, sinks) == used - 1 else vc[:, :, used - 1]
+    last[:, 0, 5], last[:, 1, 63] = float("inf"), float("-inf")
+    got = la.la_window_decode_step(q, k, v, kc.clone(), vc.clone(), posd, window, sinks=sinks)
+    hit = torch.zeros(B, Hq, d, dtype=torch.bool, device="cuda")
+    hit[:, :4, 5] = hit[:, 4:, 63] = True
+    assert (got[:, :4, 5] == float("inf")).all() and (got[:, 4:, 63] == float("-inf")).all()
+    assert torch.equal(got[~hit], want[~hit])
