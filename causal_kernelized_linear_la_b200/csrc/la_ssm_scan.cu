@@ -52,6 +52,14 @@ constexpr float kLiftSlow = 0.12f * 5.9604645e-8f * kLog2e, kLiftFast = 0.36f * 
 constexpr float kSlow = 0.003f;
 __device__ __forceinline__ float lift_limit(float a2_first, float a2_last) { return kSlow / (0.5f * fabsf(a2_first + a2_last)); }
 
+// A decay rate in log2 units.  An infinite one (a state that keeps nothing) becomes the largest finite: the
+// tokens behind a sequence in its last tile take no step, and 0 * inf is not the 0 that keeps the state.
+__device__ __forceinline__ float log2_rate(float a)
+{
+    const float r = a * kLog2e;
+    return r == -INFINITY ? -3.4028235e38f : r;
+}
+
 struct Lens {
     int use;
     int n[kMaxSeqLens];
@@ -230,8 +238,8 @@ ssm_scan_kernel(const __grid_constant__ SsmArgs a, const __grid_constant__ Lens 
         for (int i = 0; i < NS; i += 2) {
             const int s = l * NS + i;
             const float* ap = a.A + (size_t)c * a.n;
-            A2[i / 2] = pack2(mine && s < a.n ? ap[s] * kLog2e : 0.f,
-                              NS > 1 && mine && s + 1 < a.n ? ap[s + 1] * kLog2e : 0.f);
+            A2[i / 2] = pack2(mine && s < a.n ? log2_rate(ap[s]) : 0.f,
+                              NS > 1 && mine && s + 1 < a.n ? log2_rate(ap[s + 1]) : 0.f);
             const float* hp = a.h0 + ((size_t)b * a.D + c) * a.n;
             const bool from = a.h0 && mine && seg == 0;
             h[i / 2] = pack2(from && s < a.n ? hp[s] : 0.f, NS > 1 && from && s + 1 < a.n ? hp[s + 1] : 0.f);

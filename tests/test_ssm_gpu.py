@@ -362,3 +362,20 @@ def test_conv_outputs_between_the_rows_of_x(dtype):
     with pytest.raises(la.LaError) as e:
         la.la_ssm_conv(x, wt, out=far.view(-1)[:2 * N * D].view(2, N, D))
     assert e.value.code == la.LA_ERR_INVALID
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,N,ch,lens", [(2, 40, 32, [40, 7]), (1, 1500, 32, None)])     # one segment, several
+def test_scan_of_states_that_keep_nothing(dtype, B, N, ch, lens):
+    """A rate of minus infinity decays by 0, as any rate does whose decay is below the smallest number:
+    the same bits, also where a sequence ends inside a tile."""
+    p = {k: _view_cuda(v) for k, v in _scan_inputs(dtype, B, N, ch, 6, 1, True, True, True, True, False, seed=8).items()}
+    got = []
+    for rate in (-float("inf"), -1e30):
+        A = p["A"].clone()
+        A[::3, 1:4] = rate
+        got.append(la.la_ssm_scan(p["x"], p["delta"], A, p["B"], p["C"], D=p["D"], z=p["z"], delta_bias=p["delta_bias"],
+                                  delta_softplus=True, h0=p["h"], seq_lens=lens))
+    (y0, h0), (y1, h1) = got
+    assert torch.isfinite(h1).all() and torch.equal(h0, h1)
+    assert all(torch.equal(y0[b, :n], y1[b, :n]) for b, n in enumerate(lens or [N] * B))
