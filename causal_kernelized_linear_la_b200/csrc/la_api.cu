@@ -648,7 +648,7 @@ la_status la_ssm_conv(const void* x, const float* weight, const float* bias, con
         a.stream = static_cast<cudaStream_t>(cfg->stream);
         const cudaError_t err = la::launch_ssm_conv(a);
         if (err != cudaSuccess) return LA_ERR_CUDA;
-        if (b0 == 0) la::stage_mark(0, a.stream);
+        la::stage_mark(0, a.stream);
     }
     return LA_OK;
 }

@@ -297,3 +297,32 @@ def test_silu_in_fp32():
     y, _ = la.la_ssm_conv(far, torch.ones(8, 1, device="cuda"))
     y = y.flatten().tolist()
     assert y[0] == float("inf") and y[1] == far[0, 0, 1].item() and y[2:6] == [0, 0, 0, 0] and y[6] != y[6] and y[7] == 100
+
+
+def test_event_of_a_batch_of_several_launches():
+    """More sequences with lengths than one launch takes: the event lies behind the last launch.
+    The first 128 sequences hold one token each, the others all the work."""
+    B, N, ch, n = 256, 2048, 256, 16
+    lens = [1] * 128 + [N] * 128
+    r = lambda *s: torch.randn(*s, device="cuda").bfloat16()  # noqa: E731
+    x, bc, w = r(B, N, ch), r(B, N, n), torch.randn(ch, 4, device="cuda")
+    delta, A = torch.rand(B, N, ch, device="cuda").bfloat16(), -torch.rand(ch, n, device="cuda")
+    q = r(B, 2, N, 64)
+    u, y, o = torch.empty_like(x), torch.empty_like(x), torch.empty_like(q)
+    for name, call in (("conv", lambda: la.la_ssm_conv(x, w, seq_lens=lens, out=u)),
+                       ("scan", lambda: la.la_ssm_scan(x, delta, A, bc, bc, seq_lens=lens, out=y)),
+                       ("window", lambda: la.la_window_prefill(q, q, q, 256, seq_lens=lens, out=o))):
+        call()
+        start, mark, end = (torch.cuda.Event(enable_timing=True) for _ in range(3))
+        mark.record()
+        torch.cuda.synchronize()
+        la.la_set_stage_events([mark])
+        try:
+            torch.cuda._sleep(20_000_000)        # the launches queue up behind it: no host time between them
+            start.record()
+            call()
+            end.record()
+        finally:
+            la.la_set_stage_events(None)
+        torch.cuda.synchronize()
+        assert start.elapsed_time(mark) > 0.5 * start.elapsed_time(end), name
