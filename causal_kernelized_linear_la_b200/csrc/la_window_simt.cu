@@ -19,25 +19,6 @@ constexpr int kT = 64;          // queries and keys of a tile
 constexpr int kThreads = 256;   // 16 x 16
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p)
-{
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v)
-{
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
-
 template <int D, int DV>
 struct Plan {
     static constexpr int QP = D + 4, VP = DV + 4, PP = kT + 4;   // row pitches (fp32): neighbouring rows on other banks
@@ -46,7 +27,7 @@ struct Plan {
 };
 
 // grid: (query tiles, heads, sequences)
-template <typename T, int D, int DV>
+template <int D, int DV>
 __global__ void __launch_bounds__(kThreads)
 window_prefill_simt(const __grid_constant__ WindowArgs a, const __grid_constant__ WindowLens lens)
 {
@@ -64,11 +45,11 @@ window_prefill_simt(const __grid_constant__ WindowArgs a, const __grid_constant_
     KeyWalk<kT> w;
     w.init(a.k_cache != nullptr, start, a.window, a.sinks, len, q0, q1);
 
-    const T* qp = (const T*)a.q + b * a.st.q_batch + h * a.st.q_head;
+    const float* qp = (const float*)a.q + b * a.st.q_batch + h * a.st.q_head;
     for (int e = tid; e < kT * (D / 4); e += kThreads) {
         const int r = e / (D / 4), c = e % (D / 4) * 4;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (q0 + r < q1) x = load4<T>(qp + (q0 + r) * a.st.q_row + c);
+        if (q0 + r < q1) x = *reinterpret_cast<const float4*>(qp + (q0 + r) * a.st.q_row + c);
         *reinterpret_cast<float4*>(Qs + r * P::QP + c) = x;
     }
     const size_t cap = (size_t)a.window + a.sinks;
@@ -86,8 +67,8 @@ window_prefill_simt(const __grid_constant__ WindowArgs a, const __grid_constant_
     for (int it = 0; it < tiles; ++it) {
         const bool old = w.is_cache(it);
         const int base = w.base(it);
-        const T* kp = old ? (const T*)a.k_cache + (kv * cap) * D : (const T*)a.k + b * a.st.k_batch + kvh * a.st.k_head;
-        const T* vp = old ? (const T*)a.v_cache + (kv * cap) * DV : (const T*)a.v + b * a.st.v_batch + kvh * a.st.v_head;
+        const float* kp = old ? (const float*)a.k_cache + (kv * cap) * D : (const float*)a.k + b * a.st.k_batch + kvh * a.st.k_head;
+        const float* vp = old ? (const float*)a.v_cache + (kv * cap) * DV : (const float*)a.v + b * a.st.v_batch + kvh * a.st.v_head;
         const long long ks = old ? D : a.st.k_row, vs = old ? DV : a.st.v_row;
         __syncthreads();
         // keys that hold nothing are zeros here: their bits never reach a product
@@ -95,13 +76,13 @@ window_prefill_simt(const __grid_constant__ WindowArgs a, const __grid_constant_
             const int r = e / (D / 4), c = e % (D / 4) * 4;
             const bool on = old ? w.slot_held(base + r) : base + r < len;
             *reinterpret_cast<float4*>(Ks + r * P::QP + c) =
-                on ? load4<T>(kp + (base + r) * ks + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+                on ? *reinterpret_cast<const float4*>(kp + (base + r) * ks + c) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         for (int e = tid; e < kT * (DV / 4); e += kThreads) {
             const int r = e / (DV / 4), c = e % (DV / 4) * 4;
             const bool on = old ? w.slot_held(base + r) : base + r < len;
             *reinterpret_cast<float4*>(Vs + r * P::VP + c) =
-                on ? load4<T>(vp + (base + r) * vs + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+                on ? *reinterpret_cast<const float4*>(vp + (base + r) * vs + c) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         __syncthreads();
         float s[4][4];
@@ -173,7 +154,7 @@ window_prefill_simt(const __grid_constant__ WindowArgs a, const __grid_constant_
             }
         }
     }
-    T* op = (T*)a.out + b * a.st.out_batch + h * a.st.out_head;
+    float* op = (float*)a.out + b * a.st.out_batch + h * a.st.out_head;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float sum = l[i];
@@ -184,17 +165,17 @@ window_prefill_simt(const __grid_constant__ WindowArgs a, const __grid_constant_
         if (qi < q1) {
 #pragma unroll
             for (int c = 0; c < DV / 64; ++c)
-                store4(op + qi * a.st.out_row + c * 64 + tx * 4,
-                       make_float4(o[i][c * 4] * inv, o[i][c * 4 + 1] * inv, o[i][c * 4 + 2] * inv, o[i][c * 4 + 3] * inv));
+                *reinterpret_cast<float4*>(op + qi * a.st.out_row + c * 64 + tx * 4) =
+                    make_float4(o[i][c * 4] * inv, o[i][c * 4 + 1] * inv, o[i][c * 4 + 2] * inv, o[i][c * 4 + 3] * inv);
         }
     }
 }
 
-template <typename T, int D, int DV>
+template <int D, int DV>
 cudaError_t launch_simt(const WindowArgs& a)
 {
     using P = Plan<D, DV>;
-    auto kern = window_prefill_simt<T, D, DV>;
+    auto kern = window_prefill_simt<D, DV>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, P::BYTES);
     if (e != cudaSuccess) return e;
     kern<<<dim3((a.N + kT - 1) / kT, a.Hq, a.B), kThreads, P::BYTES, a.stream>>>(a, window_lens(a));
@@ -235,12 +216,8 @@ window_cache_update(const __grid_constant__ WindowArgs a, const __grid_constant_
 
 cudaError_t launch_window_prefill_simt(const WindowArgs& a)
 {
-    if (a.dtype == LA_BF16) {
-        if (a.d == 64) return a.dv == 64 ? launch_simt<__nv_bfloat16, 64, 64>(a) : launch_simt<__nv_bfloat16, 64, 128>(a);
-        return a.dv == 64 ? launch_simt<__nv_bfloat16, 128, 64>(a) : launch_simt<__nv_bfloat16, 128, 128>(a);
-    }
-    if (a.d == 64) return a.dv == 64 ? launch_simt<float, 64, 64>(a) : launch_simt<float, 64, 128>(a);
-    return a.dv == 64 ? launch_simt<float, 128, 64>(a) : launch_simt<float, 128, 128>(a);
+    if (a.d == 64) return a.dv == 64 ? launch_simt<64, 64>(a) : launch_simt<64, 128>(a);
+    return a.dv == 64 ? launch_simt<128, 64>(a) : launch_simt<128, 128>(a);
 }
 
 cudaError_t launch_window_cache_update(const WindowArgs& a)
