@@ -163,3 +163,90 @@ def test_rows_shared_by_heads_and_sequences(dtype, share):
         out += [la.la_window_decode_step(a[:, :, 7], b[:, :, 7], c[:, :, 7], kc2, vc2, pos, window, sinks=sinks), kc2, vc2]
     la.la_prefill_check()
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_state_space_rows_shared_by_sequences_and_tokens(dtype):
+    """Expanded inputs (stride 0 over sequences or tokens): the bits of copies."""
+    B, N, ch, n, G, w = 3, 70, 48, 6, 2, 4
+    g = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    x, delta, z = r(1, N, ch).expand(B, N, ch), r(B, 1, ch).expand(B, N, ch), r(1, 1, ch).expand(B, N, ch)
+    Bm, Cm = r(1, N, G, n).expand(B, N, G, n), r(B, 1, G, n).expand(B, N, G, n)
+    A, D, bias = -torch.rand(ch, n, device="cuda") - 0.1, torch.randn(ch, device="cuda"), torch.randn(ch, device="cuda") - 2
+    wt, lens = torch.randn(ch, w, device="cuda"), [70, 3, 41]
+    got, want = [], []
+    for out, f in ((got, lambda t: t), (want, lambda t: t.contiguous())):
+        y = torch.full((B, N, ch), 7.0, dtype=dtype, device="cuda")
+        out += la.la_ssm_scan(f(x), f(delta), A, f(Bm), f(Cm), D=D, z=f(z), delta_bias=bias, delta_softplus=True,
+                              seq_lens=lens, out=y)
+        h = torch.ones(B, ch, n, device="cuda")
+        out += [la.la_ssm_step(f(x)[:, 5], f(delta)[:, 5], A, f(Bm)[:, 5], f(Cm)[:, 5], h, D=D, z=f(z)[:, 5],
+                               delta_bias=bias, delta_softplus=True), h]
+        y = torch.full((B, N, ch), 7.0, dtype=dtype, device="cuda")
+        out += la.la_ssm_conv(f(x), wt, seq_lens=lens, out=y)
+        out += la.la_ssm_conv(f(delta), wt)
+        out += la.la_ssm_conv(f(z)[:, :1], wt)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_more_sequences_than_a_grid_holds(dtype):
+    """32768 sequences go in one launch: what the first and the last ones get is what they get alone."""
+    B, N, ch, n, d, window = 32768 + 5, 3, 8, 4, 64, 2
+    g = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    x, delta, bc = r(B, N, ch), r(B, N, ch).abs(), r(B, N, n)
+    A, h0, wt = -torch.rand(ch, n, device="cuda"), torch.randn(B, ch, n, device="cuda"), torch.randn(ch, 4, device="cuda")
+    q, k, v, kc, vc = r(B, 1, N, d), r(B, 1, N, d), r(B, 1, N, d), r(B, 1, window, d), r(B, 1, window, d)
+    pos = torch.arange(B, dtype=torch.int32, device="cuda") % 5
+
+    def run(s):
+        k1, v1, k2, v2, h = kc[s].clone(), vc[s].clone(), kc[s].clone(), vc[s].clone(), h0[s].clone()
+        return [*la.la_ssm_conv(x[s], wt), *la.la_ssm_scan(x[s], delta[s], A, bc[s], bc[s], h0=h0[s]),
+                la.la_ssm_step(x[s, 0], delta[s, 0], A, bc[s, 0], bc[s, 0], h), h,
+                la.la_window_prefill(q[s], k[s], v[s], window, k_cache=k1, v_cache=v1, pos=pos[s]), k1, v1,
+                la.la_window_decode_step(q[s, :, 0], k[s, :, 0], v[s, :, 0], k2, v2, pos[s], window), k2, v2]
+    whole = run(slice(0, B))
+    for s in (slice(0, 7), slice(B - 9, B)):
+        assert all(torch.equal(a[s], b) for a, b in zip(whole, run(s)))
+    la.la_prefill_check()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements in x, and in a cache: the last rows, and the first, are the right ones."""
+    N, D = (1 << 31) // 4096 + 300, 4096
+    x = torch.empty(1, N, D, dtype=torch.bfloat16, device="cuda").normal_()
+    wt, bias = torch.randn(D, 4, device="cuda"), torch.randn(D, device="cuda")
+    out, cache = la.la_ssm_conv(x, wt, bias)
+    for t0, t1 in ((0, 50), (N - 700, N)):
+        before = torch.zeros(3, D, dtype=x.dtype, device="cuda") if t0 == 0 else x[0, t0 - 3:t0]
+        ref, tol, kept = _conv_ref(x[0, t0:t1], wt, bias, before, HALF[x.dtype])
+        _check(out[0, t0:t1], ref, tol, f"tokens from {t0}")
+    assert torch.equal(cache[0], kept)
+    n, ch = 16, 4096
+    bc = torch.randn(1, N, n, device="cuda").bfloat16()
+    A = -torch.ones(ch, n, device="cuda") * 40                # a state that forgets within a few tokens
+    y, h = la.la_ssm_scan(x, x.abs_(), A, bc, bc, delta_bias=torch.ones(ch, device="cuda"), out=out)
+    tail = la.la_ssm_scan(x[:, N - 64:], x[:, N - 64:], A, bc[:, N - 64:], bc[:, N - 64:],
+                          delta_bias=torch.ones(ch, device="cuda"))
+    assert torch.equal(y[:, N - 32:], tail[0][:, 32:]) and torch.equal(h, tail[1])     # exp(-40 * 32) = 0
+    del x, out, y
+    torch.cuda.empty_cache()
+    d, cap = 128, (1 << 31) // 128 + 1000
+    kc = torch.zeros(1, 1, cap, d, dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc).normal_()
+    q = torch.zeros(1, 1, 1, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 8.0
+    far = torch.tensor([cap + 12345], dtype=torch.int32, device="cuda")       # the new token lands in a slot below
+    slot = (cap + 12345) % cap
+    for at in (0, cap // 2, cap - 700, cap - 1):
+        kc[0, 0, at, 0] = 200.0               # the score that outweighs 2^24 others: 8 * 200 * d^-0.5 = 141
+        got = la.la_window_decode_step(q[:, :, 0], q[:, :, 0] * 0, q[:, :, 0], kc, vc, far, cap)
+        assert torch.equal(got[0, 0], vc[0, 0, at]), at
+        if at == cap - 1:
+            got = la.la_window_prefill(q, q * 0, q, cap, k_cache=kc, v_cache=vc, pos=far)
+            assert torch.equal(got[0, 0, 0], vc[0, 0, at])
+        kc[0, 0, at, 0] = 0.0
+    assert torch.equal(vc[0, 0, slot], q[0, 0, 0]) and not kc[0, 0, slot].any()
+    la.la_prefill_check()
