@@ -18,15 +18,16 @@
 // clock and SM bound the scan (at n = 16 its 2^x alone take three times as
 // long as reading delta, x, z and writing y), not memory.  At 8192 tokens x 4096
 // channels x 16 states (bf16, softplus, skip, gate) those two floors are 119 and
-// 41 us; the kernel takes 264.  The recurrence warps issue in order and need about
-// 48 clocks a token where the SFU alone needs 32: without exponentials 244 us, with
-// idle helpers 199 to 217 (both measured on copies).
+// 41 us; the kernel takes 264 (fp32 271; four prompts of 4096 tokens, 3.5 waves of
+// CTAs, 529).  The recurrence warps issue in order and need about 48 clocks a
+// token where the SFU alone needs 32: without exponentials 244 us, with idle
+// helpers 199 to 217 (both measured on copies).
 //
 // Few channels leave SMs idle, so a long sequence is cut into segments: a
-// first kernel runs every segment but the last from a zero state and keeps
-// its end state and sum of dt; since the decay over a segment is
-// exp(A sum dt), each segment of the second kernel folds the segments before
-// it into its own start state and runs once more with outputs.
+// first kernel runs every segment but the last, from a zero state (the first
+// from the call's start state), and keeps its end state and sum of dt; since the
+// decay over a segment is exp(A sum dt), each segment of the second kernel folds
+// the segments before it into its own start state and runs once more with outputs.
 #include "f32x2.cuh"
 #include "la_internal.cuh"
 #include "sm100.cuh"
@@ -159,7 +160,7 @@ __device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b)
     *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
 }
 
-// Bytes of shared memory with tiles of tt tokens: the raw tiles, two prepared buffers.
+// Bytes of shared memory with tiles of tt tokens: the raw tiles, kBufs prepared buffers.
 constexpr int plan_bytes(int esize, int ns, int lanes, int tt)
 {
     const int ch = kCh, np = lanes * ns, bcp = np < 8 ? 8 : np;

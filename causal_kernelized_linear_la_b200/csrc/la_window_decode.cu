@@ -13,8 +13,10 @@
 // that takes the new token is read from the call's k and v instead.
 //
 // 64 sequences of 32 heads over 8, 4100 slots of 128 + 128
-// columns, bf16: 174 us, 93 % of the measured copy rate.  One sequence: 10.7 us, where
-// the floor is 2.6: launch, one wave of loads and the cluster's join.
+// columns, bf16: 164 to 174 us on different cards, 98 to 93 % of the measured copy rate.
+// One sequence: 10.7 us, where the floor is 2.6: launch, one wave of loads and the
+// cluster's join.  fp32: 494 us (65 %) and 53 us; a warp takes one slot a turn with
+// no load ahead and five shuffles a head, and waits for its loads.
 #include <cooperative_groups.h>
 
 #include "la_window.cuh"
@@ -179,7 +181,9 @@ window_decode_simt(const __grid_constant__ WindowArgs a, int chunks)
 //      4 c + j is column 64 c + 8 g + 2 j (+ 1).
 // No shared memory is staged: each warp keeps one block of 16 keys of K and V
 // in flight, twelve warps an SM some 90 KB.  The weights are rounded to bf16
-// for the second product (2^-8 at most, as V is held).
+// for the second product (2^-8 at most, as V is held).  A third product with what
+// the rounding took off (64 sequences of 4100 slots 168 -> 170 us) is not taken:
+// that remainder may be zero or negative, and an infinite value times it NaN.
 constexpr int kMmaHeads = 8;
 constexpr int kAhead = 2;      // blocks of a warp between an L2 prefetch and its use
 

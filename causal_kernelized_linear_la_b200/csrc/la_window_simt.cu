@@ -7,7 +7,10 @@
 // m_i and sum.  A CTA takes 64 queries of one head; a thread holds 4 x 4 scores
 // and 4 rows of dv / 16 output columns in registers, so each 16-byte read of
 // shared memory feeds 8 (scores) to 16 (outputs) FMAs.
-// Bound by the FMA pipe and shared-memory reads: about 24 TFLOP/s.
+// A 16384-token prompt (32 heads of 128, window 4096) takes 39.5 ms: 24 TFLOP/s, a
+// third of the FMA pipe's 73.  Its 119 KB of shared memory leave one CTA, two
+// warps a scheduler, which do not cover the waits for key tiles (no loads ahead),
+// shared-memory reads and barriers: issue slots are 45 % busy, the FMA pipe 35 %.
 #include <algorithm>
 
 #include "la_window.cuh"

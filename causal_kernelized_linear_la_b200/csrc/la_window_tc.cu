@@ -30,8 +30,10 @@
 // of tiles takes about 3700 clocks where the pipe needs 2060: a tile's own chain
 // (load of the scores 350, maximum 250, exponentials 1100 and more while the
 // other tile uses the SFU too, products 1024, hand-offs) is longer than what the
-// other tile hides.  A 16384-token prompt (32 heads of 128, window 4096) runs at
-// 950 to 1090 TFLOP/s, at the card's 1000 W limit.  Measured and not kept: two
+// other tile hides: the tensor pipe is active 52 % of the time, the SFU 52 %.  A
+// 16384-token prompt (32 heads of 128, window 4096) takes 987 to 1008 us on
+// different cards, 955 to 976 TFLOP/s at the 1000 W limit; a chunk of 4096 tokens
+// behind 65540 cached slots 4.3 ms (1020 TFLOP/s).  Measured and not kept: two
 // threads a query (1021 against 1014 us), an issuing warp a tile (1012), a
 // quarter of the exponentials as polynomials on the FMA pipe (1033 to 1180).
 #include <cudaTypedefs.h>
