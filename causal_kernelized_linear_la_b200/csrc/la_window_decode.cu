@@ -13,7 +13,7 @@
 // that takes the new token is read from the call's k and v instead.
 //
 // 64 sequences of 32 heads over 8, 4100 slots of 128 + 128
-// columns, bf16: 164 to 174 us on different cards, 98 to 93 % of the measured copy rate.
+// columns, bf16: 163 to 179 us on different cards, 98 to 90 % of the measured copy rate.
 // One sequence: 10.7 us, where the floor is 2.6: launch, one wave of loads and the
 // cluster's join.  fp32: 494 us (65 %) and 53 us; a warp takes one slot a turn with
 // no load ahead and five shuffles a head, and waits for its loads.
@@ -180,10 +180,10 @@ window_decode_simt(const __grid_constant__ WindowArgs a, int chunks)
 //      2t+9; byte permutes pair the keys, and row g (g + 8) of output tile
 //      4 c + j is column 64 c + 8 g + 2 j (+ 1).
 // No shared memory is staged: each warp keeps one block of 16 keys of K and V
-// in flight, twelve warps an SM some 90 KB.  The weights are rounded to bf16
-// for the second product (2^-8 at most, as V is held).  A third product with what
-// the rounding took off (64 sequences of 4100 slots 168 -> 170 us) is not taken:
-// that remainder may be zero or negative, and an infinite value times it NaN.
+// in flight, twelve warps an SM some 90 KB.  The weights meet V as two bf16
+// parts, two products that keep 2^-16 of each weight: beside the loads the second
+// costs 1 to 2 % (64 sequences of 4100 slots 168 -> 170 us on one card, 176 -> 179 on
+// another), while weights rounded to one bf16 took the error against exact weights from 0.0017 of the output to 0.0021.
 constexpr int kMmaHeads = 8;
 constexpr int kAhead = 2;      // blocks of a warp between an L2 prefetch and its use
 
@@ -212,6 +212,18 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b)
 {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two weights' upper bf16 halves (cut off, not rounded), and what that leaves of them.  The rest is
+// at least 1e-30, far below anything that counts: a rest of zero would make an infinite value NaN.
+__device__ __forceinline__ uint32_t upper_pair(float a, float b)
+{
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ uint32_t lower_pair(float a, float b)
+{
+    auto rest = [](float x) { return fmaxf(x - __uint_as_float(__float_as_uint(x) & 0xffff0000u), 1e-30f); };
+    return bf16_pair(rest(a), rest(b));
 }
 
 // grid: (splits, Hkv * head chunks, sequences), clusters along x
@@ -346,7 +358,8 @@ window_decode_mma(const __grid_constant__ WindowArgs a, int chunks)
 #pragma unroll
                     for (int x = 0; x < VC; ++x) vr[i][x] = make_uint4(0u, 0u, 0u, 0u);
         }
-        const uint32_t p0 = transpose8(bf16_pair(c[0], c[1])), p1 = transpose8(bf16_pair(c[2], c[3]));
+        const uint32_t p0 = transpose8(upper_pair(c[0], c[1])), p1 = transpose8(upper_pair(c[2], c[3]));
+        const uint32_t r0 = transpose8(lower_pair(c[0], c[1])), r1 = transpose8(lower_pair(c[2], c[3]));
 #pragma unroll
         for (int x = 0; x < VC; ++x) {
             const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vr[0][x]);
@@ -354,9 +367,12 @@ window_decode_mma(const __grid_constant__ WindowArgs a, int chunks)
             const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vr[2][x]);
             const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vr[3][x]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                mma_16816(o[4 * x + j], __byte_perm(v0[j], v1[j], 0x5410), __byte_perm(v0[j], v1[j], 0x7632),
-                          __byte_perm(v2[j], v3[j], 0x5410), __byte_perm(v2[j], v3[j], 0x7632), p0, p1);
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a0 = __byte_perm(v0[j], v1[j], 0x5410), a1 = __byte_perm(v0[j], v1[j], 0x7632),
+                               a2 = __byte_perm(v2[j], v3[j], 0x5410), a3 = __byte_perm(v2[j], v3[j], 0x7632);
+                mma_16816(o[4 * x + j], a0, a1, a2, a3, p0, p1);
+                mma_16816(o[4 * x + j], a0, a1, a2, a3, r0, r1);
+            }
         }
         if (next < s1) load_v(next);
     }

@@ -481,7 +481,9 @@ LA_API la_status la_window_prefill(const void* q, const void* k, const void* v, 
  * value into the cache's slot of position pos[b] and attends over the cache.
  *
  *   q [B,Hq,d], k [B,Hkv,d], v [B,Hkv,dv], out [B,Hq,dv]; caches and pos
- *   (required) as above.  One kernel, no workspace.
+ *   (required) as above.  One kernel, no workspace.  bf16 keeps each weight w_ij
+ *   as two bf16 parts (to 2^-15 of it); every slot in use is seen, and a value
+ *   there may be infinite.
  */
 LA_API la_status la_window_decode_step(const void* q, const void* k, const void* v, void* out,
                                        void* k_cache, void* v_cache, const int* pos,

@@ -343,3 +343,27 @@ def test_decode_infinite_value_in_the_last_slot(dtype, cap, pos):
     hit[:, :4, 5] = hit[:, 4:, 63] = True
     assert (got[:, :4, 5] == float("inf")).all() and (got[:, 4:, 63] == float("-inf")).all()
     assert torch.equal(got[~hit], want[~hit])
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,d,dv,window,sinks,pos", [
+    (2, 16, 2, 128, 128, 700, 5, [704, 2000]),
+    (40, 32, 8, 64, 64, 400, 4, [100 + 7 * b for b in range(40)]),
+    (80, 16, 8, 64, 128, 97, 3, [50 + b for b in range(80)]),
+])
+def test_decode_keeps_the_weights(B, Hq, Hkv, d, dv, window, sinks, pos):
+    """bf16 token steps take each weight as two bf16 parts: the upper one cut off, so the rest is
+    below 2^-7 of it, and that rest rounded by 2^-8 of itself.  2^-15 of the weights is what is
+    lost, where one rounding would take 2^-8; the other terms are those of fp32 inputs."""
+    g = torch.Generator().manual_seed(B)
+    r = lambda *s: torch.randn(*s, generator=g).bfloat16().cuda()  # noqa: E731
+    cap = window + sinks
+    q, k, v, kc, vc = r(B, Hq, d), r(B, Hkv, d), r(B, Hkv, dv), r(B, Hkv, cap, d), r(B, Hkv, cap, dv)
+    o = la.la_window_decode_step(q, k, v, kc, vc, torch.tensor(pos, dtype=torch.int32, device="cuda"), window, sinks=sinks)
+    o, q, kc, vc = _f64(o), _f64(q), _f64(kc), _f64(vc)
+    for b in range(B):
+        used = min(pos[b] + 1, cap)       # the slots in use are all seen, in any order
+        for h in range(Hq):
+            K, V = kc[b, h // (Hq // Hkv), :used], vc[b, h // (Hq // Hkv), :used]
+            ref, tol = _ref(q[b, h:h + 1], K, V, used - 1, used, 0, d ** -0.5, torch.float32)
+            spread, _ = _ref(q[b, h:h + 1], K, np.abs(V), used - 1, used, 0, d ** -0.5, torch.float32)
+            _check(o[b, h:h + 1], ref, tol + 2.0 ** -15 * spread + 2.0 ** -8 * np.abs(ref), f"sequence {b} head {h}")
