@@ -180,10 +180,10 @@ window_decode_simt(const __grid_constant__ WindowArgs a, int chunks)
 //      2t+9; byte permutes pair the keys, and row g (g + 8) of output tile
 //      4 c + j is column 64 c + 8 g + 2 j (+ 1).
 // No shared memory is staged: each warp keeps one block of 16 keys of K and V
-// in flight, twelve warps an SM some 90 KB.  The weights meet V as two bf16
-// parts, two products that keep 2^-16 of each weight: beside the loads the second
-// costs 1 to 2 % (64 sequences of 4100 slots 168 -> 170 us on one card, 176 -> 179 on
-// another), while weights rounded to one bf16 took the error against exact weights from 0.0017 of the output to 0.0021.
+// in flight, twelve warps an SM some 90 KB.  The weights meet V as two bf16 parts,
+// two products that keep 2^-15 of each weight: beside the loads the second costs 1
+// to 2 % (64 sequences of 4100 slots 168 -> 170 us on one card, 176 -> 179 on another),
+// while weights rounded to one bf16 took the error from 0.0017 of the output to 0.0021.
 constexpr int kMmaHeads = 8;
 constexpr int kAhead = 2;      // blocks of a warp between an L2 prefetch and its use
 
@@ -257,8 +257,8 @@ window_decode_mma(const __grid_constant__ WindowArgs a, int chunks)
     const float sl = a.scale * kLog2e;
 
     uint4 kr[2][KS], vr[4][VC];
-    // slots past the run repeat its last one; their weights are zero, and so are their values by the time
-    // they are used: the last slot's may be infinite
+    // slots past the run repeat its last one; their scores are -inf, and their values zero by the time they
+    // meet the weights: the last slot's may be infinite
     auto k_row = [&](int s) { const int x = min(s, s1 - 1); return (x == slot_new ? kn : kc + (size_t)x * D) + 8 * t; };
     auto v_row = [&](int s) { const int x = min(s, s1 - 1); return (x == slot_new ? vn : vc + (size_t)x * DV) + 8 * g; };
     auto load_k = [&](int s) {

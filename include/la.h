@@ -502,7 +502,8 @@ LA_API la_status la_window_decode_step(const void* q, const void* k, const void*
  * part; la_ssm_scan = segment summaries, if it needs a workspace, and the scan;
  * la_window_prefill = attention and, with a cache, the cache's update; every
  * other path, la_causal_conv included, one kernel; a batch with lengths of more
- * than 128 sequences runs as several such launches).  events are cudaEvent_t handles
+ * than 128 sequences runs as several such launches, and an event then lies behind
+ * the last of them).  events are cudaEvent_t handles
  * owned by the caller, who must keep them alive while the hook is set; n = 0
  * turns it off.  The setting is process-wide and not thread-safe: set it
  * only while no other thread launches through this library.  Returns

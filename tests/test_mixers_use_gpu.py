@@ -326,3 +326,36 @@ def test_event_of_a_batch_of_several_launches():
             la.la_set_stage_events(None)
         torch.cuda.synchronize()
         assert start.elapsed_time(mark) > 0.5 * start.elapsed_time(end), name
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_empty_calls(dtype):
+    """No sequences, no tokens, no channels, sequences of length zero: nothing but what the formulas leave."""
+    r = lambda *s: torch.randn(*s, device="cuda").to(dtype)  # noqa: E731
+    A, w, h0 = -torch.rand(16, 4, device="cuda"), torch.randn(16, 4, device="cuda"), torch.randn(2, 16, 4, device="cuda")
+    for B, N, lens in ((0, 5, None), (2, 0, None), (2, 5, [0, 0])):
+        x, bc, c0 = r(B, N, 16), r(B, N, 4), r(B, 3, 16)
+        out = torch.full_like(x, 7.0)
+        y, h = la.la_ssm_scan(x, x, A, bc, bc, h0=h0[:B].contiguous(), seq_lens=lens, out=out)
+        assert torch.equal(h, h0[:B]) and (y == 7.0).all()
+        y, h = la.la_ssm_scan(x, x, A, bc, bc, seq_lens=lens, out=out)
+        assert not h.any() and (y == 7.0).all()
+        u, c = la.la_ssm_conv(x, w, cache=c0, seq_lens=lens, out=out)
+        assert torch.equal(c, c0) and (u == 7.0).all()
+        q, kc = r(B, 2, N, 64), r(B, 2, 9, 64)
+        vc, o = r(B, 2, 9, 64), torch.full((B, 2, N, 64), 7.0, dtype=dtype, device="cuda")
+        k0, v0, pos = kc.clone(), vc.clone(), torch.full((B,), 6, dtype=torch.int32, device="cuda")
+        la.la_window_prefill(q, q, q, 8, sinks=1, k_cache=kc, v_cache=vc, pos=pos, seq_lens=lens, out=o)
+        assert (o == 7.0).all() and torch.equal(kc, k0) and torch.equal(vc, v0)
+    x, bc = r(0, 16), r(0, 4)
+    assert la.la_ssm_step(x, x, A, bc, bc, h0[:0]).shape == (0, 16)
+    e = r(0, 2, 64)
+    assert la.la_window_decode_step(e, e, e, r(0, 2, 9, 64), r(0, 2, 9, 64), torch.zeros(0, dtype=torch.int32, device="cuda"),
+                                    8, sinks=1).shape == (0, 2, 64)
+    x = r(2, 5, 0)
+    y, h = la.la_ssm_scan(x, x, A[:0], r(2, 5, 4), r(2, 5, 4))
+    assert y.shape == (2, 5, 0) and h.shape == (2, 0, 4)
+    u, c = la.la_ssm_conv(x, w[:0])
+    assert u.shape == (2, 5, 0) and c.shape == (2, 3, 0)
+    torch.cuda.synchronize()
+    la.la_prefill_check()
